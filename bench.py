@@ -48,10 +48,14 @@ def log(msg):
     print(msg, file=sys.stderr, flush=True)
 
 
+# the sources of the kernels that the counter summaries in profiles/ measured
+PROFILED_SOURCES = ("api.cpp", "common.hpp", "gemm_bf16.hip", "gemm_mx.hip", "launch.hpp", "pipeline.hpp", "quantize.hip")
+
+
 def kernel_source_hash() -> str:
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "moe_expert_grouped_gemm_amd", "csrc")
-    for f in sorted(os.listdir(csrc)):
+    for f in PROFILED_SOURCES:
         with open(os.path.join(csrc, f), "rb") as fh:
             h.update(f.encode() + fh.read())
     return h.hexdigest()[:16]
