@@ -75,8 +75,10 @@ typedef enum {
     PT_FP8_E4M3 = 3,         /* E4M3 codes with one fp32 scale per tensor (current
                                 scaling, pt_fp8_quantize): the scale arguments point
                                 to fp32 factors, one for A and one per expert for B */
-    PT_FP8_E4M3_ROWWISE = 4  /* E4M3 codes with one fp32 scale per row of A [M] and per
+    PT_FP8_E4M3_ROWWISE = 4, /* E4M3 codes with one fp32 scale per row of A [M] and per
                                 row of B [G, N] (pt_fp8_quantize_rows) */
+    PT_FP32 = 5              /* 32-bit floats: the residual stream and the router's logits
+                                (no operand of the grouped GEMMs) */
 } pt_dtype;
 
 typedef enum {
@@ -94,8 +96,17 @@ typedef enum {
     PT_OP_DGRAD_SWIGLU = 3   /* pt_grouped_gemm_dgrad_swiglu (for pt_gemm_config_of) */
 } pt_op;
 
+typedef enum {
+    PT_GATE_SOFTMAX = 0,     /* scores are the logits, weights their softmax           */
+    PT_GATE_SIGMOID = 1      /* scores are sigmoid(logit) + bias, weights the sigmoids */
+} pt_gate;
+
 /* Largest expert count one call accepts. */
 #define PT_MAX_GROUPS 1024
+/* Most experts per token that the router chooses. */
+#define PT_MAX_TOPK 16
+/* Most tokens that one call of pt_moe_few_tokens takes. */
+#define PT_FEW_TOKENS 64
 
 /*
  * Grouped forward: for every expert g and each of its rows r,
@@ -577,6 +588,133 @@ size_t pt_grouped_gemm_workspace_size(int op, int64_t G, int64_t M, int64_t N,
                                       int64_t K, int dtype);
 
 /*
+ * RMS norm of the residual stream, with the operand of the next grouped GEMM
+ * in 8 bits: for each row r
+ *     h[r]    = x[r] + residual[r]      rounded once to the stream's type
+ *     rstd[r] = 1 / sqrt(mean(h[r]^2) + eps)                        (fp32)
+ *     v[r, c] = h[r, c] * rstd[r] * weight[c]                       (fp32)
+ *     y[r]    = bf16(v[r]),   q[r] = codes of v[r]
+ * The codes are those of the unrounded v, by the rules of pt_mx_quantize and
+ * pt_fp8_quantize_rows, so a code is one rounding away from v, not two.
+ *  x            [rows, cols] bf16: the last sublayer's output
+ *  residual     [rows, cols] of stream_dtype, or NULL (h = x)
+ *  weight       [cols] bf16
+ *  residual_out [rows, cols] of stream_dtype: h, the stream of the next
+ *               sublayer (may be residual itself); NULL only where residual is
+ *  y            [rows, cols] bf16, or NULL where codes are asked for
+ *  q, scales    code_dtype PT_MXFP8_E4M3: codes [rows, cols] and E8M0
+ *               [rows, cols/32]; PT_FP8_E4M3_ROWWISE: codes and fp32 [rows]
+ *               (the factor that multiplies the codes back); PT_BF16: no
+ *               codes, both NULL
+ *  rstd         [rows] fp32 for the backward, or NULL
+ *  stream_dtype PT_BF16 or PT_FP32
+ * A row of zeros has rstd = eps^-1/2 and zero outputs (block exponent 0, row
+ * factor 1).  A row that holds a NaN or an infinity gives NaNs in y and in
+ * its codes.
+ *  Requirements: cols % 8 == 0 (cols % 32 == 0 for MXFP8), cols <= 32768,
+ *  rows <= 2^23, eps >= 0; x, residual, weight, residual_out, y and q 16-byte
+ *  aligned.
+ */
+int pt_rmsnorm_fwd(const void *x, const void *residual, const void *weight, void *residual_out, void *y, void *q,
+                   void *scales, float *rstd, int64_t rows, int64_t cols, float eps, int stream_dtype, int code_dtype,
+                   void *stream);
+
+/*
+ * Its backward, the codes taken as v itself.  With xhat = s * rstd and
+ * g = dy * weight, for each row
+ *     ds[r]   = dres[r] + rstd[r] * (g[r] - xhat[r] * mean(g[r] * xhat[r]))
+ *     dweight = (accumulate ? dweight : 0) + sum over rows of dy[r] * xhat[r]
+ * ds is the gradient of x and of residual alike.
+ *  dy           [rows, cols] bf16;  s the forward's residual_out;  rstd its
+ *  dres         [rows, cols] of stream_dtype: the gradient that reaches the
+ *               stream past this norm, or NULL (none)
+ *  ds           [rows, cols] of stream_dtype (may be dres itself)
+ *  dweight      [cols] fp32, or NULL where it is not wanted
+ *  workspace    pt_rmsnorm_workspace_size(rows, cols) bytes, 16-byte aligned,
+ *               where dweight is wanted (0 bytes for few rows): partial sums,
+ *               added in a fixed order, so results are deterministic
+ *  Requirements as pt_rmsnorm_fwd; dy, s, weight, dres, ds and dweight
+ *  16-byte aligned.
+ */
+int pt_rmsnorm_bwd(const void *dy, const void *s, const void *weight, const float *rstd, const void *dres, void *ds,
+                   float *dweight, int64_t rows, int64_t cols, int stream_dtype, int accumulate, void *workspace,
+                   size_t workspace_bytes, void *stream);
+size_t pt_rmsnorm_workspace_size(int64_t rows, int64_t cols);
+
+/*
+ * The router: for each token the k experts with the largest scores (ties to
+ * the lower index) and their weights, and the chosen pairs' order by expert --
+ * the lens and row order that the grouped GEMMs take.
+ *  PT_GATE_SOFTMAX  scores are the logits; weight = softmax over all E
+ *                   experts, or with renorm over the chosen ones
+ *  PT_GATE_SIGMOID  score = sigmoid(logit) + bias, rounded to fp32 once;
+ *                   weight = sigmoid(logit) (no bias), with renorm divided by
+ *                   the sum over the chosen ones
+ * and every weight times `scale`.  An expert whose logit is -inf or NaN is not
+ * chosen (a NaN also sets error bit 4); a token with fewer than k experts left
+ * gets id -1 and weight 0 in the slots past them.
+ *  logits       [T, E] fp32 or bf16 (logits_dtype PT_FP32 or PT_BF16)
+ *  bias         [E] fp32 (PT_GATE_SIGMOID only), or NULL
+ *  topk_ids     [T, k] int32, largest score first;  topk_weights [T, k] fp32
+ *  lens         [E] int64: pairs per expert (group_lens of the grouped GEMMs)
+ *  row_of       [T, k] int32: the pair's row in expert order, tokens in their
+ *               order inside an expert; -1 for id -1
+ *  token_of     [T * k] int32: the token of each row; -1 past the last row
+ * so A[r] = x[token_of[r]], and out[t] = sum_j topk_weights[t, j] *
+ * Y[row_of[t, j]].  sum(lens) < T * k where an id is -1: pass group_offs, or M
+ * = sum(lens).
+ *  workspace    optional for at most 64 tokens, else required:
+ *               pt_moe_route_workspace_size(T, E, k) bytes, 4-byte aligned
+ *               (word 0 takes the error bits)
+ *  Requirements: 1 <= k <= E, E <= PT_MAX_GROUPS, k <= PT_MAX_TOPK, T <= 2^23;
+ *  logits 16-byte aligned.
+ */
+int pt_moe_route(const void *logits, const float *bias, int32_t *topk_ids, float *topk_weights, int64_t *lens,
+                 int32_t *row_of, int32_t *token_of, int64_t T, int64_t E, int64_t k, int logits_dtype, int gate,
+                 int renorm, float scale, void *workspace, size_t workspace_bytes, void *stream);
+size_t pt_moe_route_workspace_size(int64_t T, int64_t E, int64_t k);
+
+/*
+ * The gradient of the logits from the gradient of the weights (the choice
+ * itself and the bias have none).
+ *  topk_ids  [T, k] as pt_moe_route returned them: slots with id -1 (or any id
+ *            outside [0, E)) give nothing
+ *  dweights  [T, k] fp32;  dlogits [T, E] of logits_dtype, every element
+ *            written (0 for an expert without gradient)
+ *  The other arguments are the forward's.
+ */
+int pt_moe_route_bwd(const void *logits, const int32_t *topk_ids, const float *dweights, void *dlogits, int64_t T,
+                     int64_t E, int64_t k, int logits_dtype, int gate, int renorm, float scale, void *stream);
+
+/*
+ * A whole MoE layer for a few tokens (decoding, T <= PT_FEW_TOKENS): the
+ * router of pt_moe_route, and for each token t
+ *     out[t] = bf16( sum over its slots j of topk_weights[t, j] *
+ *                    (bf16(silu(gate) * up) . w2[e]^T) ),  e = topk_ids[t, j],
+ *     [gate | up] = x[t] . w1[e]^T
+ * with fp32 sums and the SwiGLU (and swiglu_limit) of pt_grouped_gemm_fwd's
+ * PT_EPI_SWIGLU.  Only the chosen experts' weights are read.  A token without
+ * experts gives zeros.
+ *  x     [T, H] bf16;  logits [T, E];  out [T, H] bf16
+ *  w1    [E, 2I, H], w2 [E, H, I]: bf16 (weight_dtype PT_BF16, scales NULL),
+ *        or codes with E8M0 scales [E, 2I, H/32] and [E, H, I/32]
+ *        (PT_MXFP8_E4M3, PT_MXFP4_E2M1: the layouts of pt_grouped_gemm_fwd
+ *        with trans_b = 1)
+ *  topk_ids, topk_weights [T, k]: the router's, as outputs
+ *  workspace  required: pt_moe_few_tokens_workspace_size(T, E, H, I, k) bytes,
+ *        16-byte aligned (word 0 takes the error bits)
+ *  Deterministic.  Requirements: H and I % 8 == 0 (bf16) or % 32 == 0 (MX),
+ *  H and I <= 16384; x, logits, w1, w2 and out 16-byte aligned; the others as
+ *  pt_moe_route.  A weight tensor may exceed 2 GiB.
+ */
+int pt_moe_few_tokens(const void *x, const void *logits, const float *bias, const void *w1, const uint8_t *w1_scale,
+                      const void *w2, const uint8_t *w2_scale, void *out, int32_t *topk_ids, float *topk_weights,
+                      int64_t T, int64_t E, int64_t H, int64_t I, int64_t k, int logits_dtype, int gate, int renorm,
+                      float scale, int weight_dtype, float swiglu_limit, void *workspace, size_t workspace_bytes,
+                      void *stream);
+size_t pt_moe_few_tokens_workspace_size(int64_t T, int64_t E, int64_t H, int64_t I, int64_t k);
+
+/*
  * Kernel configurations and tuning (the Primus-Turbo README, "What's New":
  * grouped GEMM autotune).  A configuration of one grouped GEMM call is a
  * number 0..3: bit 0 takes tiles in the static order even when the
@@ -623,7 +761,8 @@ void pt_clear_gemm_tuning(void);
  * do not sum to M; with group_offs, two experts' ranges overlap or come out
  * of expert order, offs[g] + lens[g] > offs[g + 1], or offs[G] lies outside
  * [0, M]) and by the expert-weight kernels (bit 3: an expert address was
- * NULL or not 16-byte aligned).  Rows between experts' ranges that no
+ * NULL or not 16-byte aligned) and by the router (bit 4: a logit, or its score
+ * with the bias, was NaN).  Rows between experts' ranges that no
  * expert owns (explicit offsets with gaps) are valid input and set no bit:
  * the forward and data gradient leave them unwritten, the weight gradient
  * and the token quantiser do not read them.

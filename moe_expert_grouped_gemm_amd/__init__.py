@@ -29,6 +29,10 @@ __all__ = [
     "pt_stack_experts", "pt_mx_quantize_experts", "expert_addresses",
     "pt_set_gemm_config", "pt_gemm_config_of", "pt_clear_gemm_tuning", "PT_CONFIG_RULES", "PT_CONFIG_TUNE",
     "PT_OP_DGRAD_SWIGLU", "PT_MAX_GROUPS",
+    "pt_rmsnorm_fwd", "pt_rmsnorm_bwd", "pt_rmsnorm_workspace_size",
+    "pt_moe_route", "pt_moe_route_bwd", "pt_moe_route_workspace_size",
+    "pt_moe_few_tokens", "pt_moe_few_tokens_workspace_size",
+    "PT_FP32", "PT_GATE_SOFTMAX", "PT_GATE_SIGMOID", "PT_MAX_TOPK", "PT_FEW_TOKENS",
     "pt_grouped_gemm_workspace_size", "pt_read_error_flags", "pt_status_string", "pt_version",
 ]
 
@@ -37,6 +41,9 @@ PT_EPI_NONE, PT_EPI_SWIGLU, PT_EPI_SWIGLU_MXFP4 = 0, 1, 2
 PT_OP_FWD, PT_OP_DGRAD, PT_OP_WGRAD, PT_OP_DGRAD_SWIGLU = 0, 1, 2, 3
 PT_CONFIG_RULES, PT_CONFIG_TUNE = -1, -2
 PT_MAX_GROUPS = 1024
+PT_FP32 = 5
+PT_GATE_SOFTMAX, PT_GATE_SIGMOID = 0, 1
+PT_MAX_TOPK, PT_FEW_TOKENS = 16, 64
 
 EXPORTS = (
     "pt_grouped_gemm_fwd", "pt_grouped_gemm_dgrad", "pt_grouped_gemm_dgrad_swiglu", "pt_grouped_gemm_wgrad",
@@ -44,6 +51,9 @@ EXPORTS = (
     "pt_grouped_gemm_fwd_pitched", "pt_mx_quantize", "pt_mx_quantize_pitched", "pt_mx_quantize_t", "pt_mx_quantize_tokens", "pt_fp8_quantize", "pt_fp8_quantize_rows",
     "pt_stack_experts", "pt_mx_quantize_experts",
     "pt_set_gemm_config", "pt_gemm_config_of", "pt_clear_gemm_tuning",
+    "pt_rmsnorm_fwd", "pt_rmsnorm_bwd", "pt_rmsnorm_workspace_size",
+    "pt_moe_route", "pt_moe_route_bwd", "pt_moe_route_workspace_size",
+    "pt_moe_few_tokens", "pt_moe_few_tokens_workspace_size",
     "pt_grouped_gemm_workspace_size", "pt_read_error_flags", "pt_status_string", "pt_version",
 )
 
@@ -110,6 +120,23 @@ def load(require_gpu: bool = True):
     L.pt_gemm_config_of.argtypes = [i32, i32, i32, i32, i64, i64, i64, i64]
     L.pt_clear_gemm_tuning.restype = None
     L.pt_clear_gemm_tuning.argtypes = []
+    L.pt_rmsnorm_fwd.restype = i32
+    L.pt_rmsnorm_fwd.argtypes = [p, p, p, p, p, p, p, p, i64, i64, f32, i32, i32, p]
+    L.pt_rmsnorm_bwd.restype = i32
+    L.pt_rmsnorm_bwd.argtypes = [p, p, p, p, p, p, p, i64, i64, i32, i32, p, sz, p]
+    L.pt_rmsnorm_workspace_size.restype = sz
+    L.pt_rmsnorm_workspace_size.argtypes = [i64, i64]
+    L.pt_moe_route.restype = i32
+    L.pt_moe_route.argtypes = [p, p, p, p, p, p, p, i64, i64, i64, i32, i32, i32, f32, p, sz, p]
+    L.pt_moe_route_bwd.restype = i32
+    L.pt_moe_route_bwd.argtypes = [p, p, p, p, i64, i64, i64, i32, i32, i32, f32, p]
+    L.pt_moe_route_workspace_size.restype = sz
+    L.pt_moe_route_workspace_size.argtypes = [i64, i64, i64]
+    L.pt_moe_few_tokens.restype = i32
+    L.pt_moe_few_tokens.argtypes = [p, p, p, p, p, p, p, p, p, p, i64, i64, i64, i64, i64, i32, i32, i32, f32, i32, f32,
+                                    p, sz, p]
+    L.pt_moe_few_tokens_workspace_size.restype = sz
+    L.pt_moe_few_tokens_workspace_size.argtypes = [i64, i64, i64, i64, i64]
     L.pt_grouped_gemm_workspace_size.argtypes = [i32, i64, i64, i64, i64, i32]
     L.pt_read_error_flags.restype = i32
     L.pt_read_error_flags.argtypes = [p, p, ctypes.POINTER(ctypes.c_uint32)]
@@ -280,6 +307,60 @@ def pt_mx_quantize_experts(experts, q, scales, q_t, scales_t, G, rows, cols, dty
     _check("pt_mx_quantize_experts", L.pt_mx_quantize_experts(
         _ptr(experts), _ptr(q), _ptr(scales), _ptr(q_t), _ptr(scales_t), G, rows, cols, dtype,
         _ptr(workspace), _nbytes(workspace), _stream(stream)))
+
+
+def pt_rmsnorm_fwd(x, residual, weight, residual_out, y, q, scales, rstd, rows, cols, eps, stream_dtype=PT_BF16,
+                   code_dtype=PT_BF16, stream=None):
+    L = load()
+    _check("pt_rmsnorm_fwd", L.pt_rmsnorm_fwd(
+        _ptr(x), _ptr(residual), _ptr(weight), _ptr(residual_out), _ptr(y), _ptr(q), _ptr(scales), _ptr(rstd),
+        rows, cols, eps, stream_dtype, code_dtype, _stream(stream)))
+
+
+def pt_rmsnorm_bwd(dy, s, weight, rstd, dres, ds, dweight, rows, cols, stream_dtype=PT_BF16, accumulate=0,
+                   workspace=None, stream=None):
+    L = load()
+    _check("pt_rmsnorm_bwd", L.pt_rmsnorm_bwd(
+        _ptr(dy), _ptr(s), _ptr(weight), _ptr(rstd), _ptr(dres), _ptr(ds), _ptr(dweight), rows, cols, stream_dtype,
+        accumulate, _ptr(workspace), _nbytes(workspace), _stream(stream)))
+
+
+def pt_rmsnorm_workspace_size(rows, cols) -> int:
+    return int(load(require_gpu=False).pt_rmsnorm_workspace_size(rows, cols))
+
+
+def pt_moe_route(logits, bias, topk_ids, topk_weights, lens, row_of, token_of, T, E, k, logits_dtype=PT_FP32,
+                 gate=PT_GATE_SOFTMAX, renorm=1, scale=1.0, workspace=None, stream=None):
+    L = load()
+    _check("pt_moe_route", L.pt_moe_route(
+        _ptr(logits), _ptr(bias), _ptr(topk_ids), _ptr(topk_weights), _ptr(lens), _ptr(row_of), _ptr(token_of),
+        T, E, k, logits_dtype, gate, renorm, scale, _ptr(workspace), _nbytes(workspace), _stream(stream)))
+
+
+def pt_moe_route_workspace_size(T, E, k) -> int:
+    return int(load(require_gpu=False).pt_moe_route_workspace_size(T, E, k))
+
+
+def pt_moe_route_bwd(logits, topk_ids, dweights, dlogits, T, E, k, logits_dtype=PT_FP32, gate=PT_GATE_SOFTMAX,
+                     renorm=1, scale=1.0, stream=None):
+    L = load()
+    _check("pt_moe_route_bwd", L.pt_moe_route_bwd(
+        _ptr(logits), _ptr(topk_ids), _ptr(dweights), _ptr(dlogits), T, E, k, logits_dtype, gate, renorm, scale,
+        _stream(stream)))
+
+
+def pt_moe_few_tokens(x, logits, bias, w1, w1_scale, w2, w2_scale, out, topk_ids, topk_weights, T, E, H, I, k,
+                      logits_dtype=PT_FP32, gate=PT_GATE_SOFTMAX, renorm=1, scale=1.0, weight_dtype=PT_BF16,
+                      workspace=None, stream=None, swiglu_limit=0.0):
+    L = load()
+    _check("pt_moe_few_tokens", L.pt_moe_few_tokens(
+        _ptr(x), _ptr(logits), _ptr(bias), _ptr(w1), _ptr(w1_scale), _ptr(w2), _ptr(w2_scale), _ptr(out),
+        _ptr(topk_ids), _ptr(topk_weights), T, E, H, I, k, logits_dtype, gate, renorm, scale, weight_dtype,
+        swiglu_limit, _ptr(workspace), _nbytes(workspace), _stream(stream)))
+
+
+def pt_moe_few_tokens_workspace_size(T, E, H, I, k) -> int:
+    return int(load(require_gpu=False).pt_moe_few_tokens_workspace_size(T, E, H, I, k))
 
 
 def pt_set_gemm_config(config) -> int:

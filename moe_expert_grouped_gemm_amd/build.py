@@ -7,7 +7,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libptgg.so")
 OBJ = os.path.join(HERE, "_build")
-SOURCES = ["api.cpp", "gemm_bf16.hip", "gemm_mx.hip", "quantize.hip"]
+SOURCES = ["api.cpp", "gemm_bf16.hip", "gemm_mx.hip", "quantize.hip", "norm.hip", "route.hip",
+           "few_tokens.hip", "layer_api.cpp"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 # Packed-fp32 VALU forms are switched off for all device code.
 FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
