@@ -71,8 +71,11 @@ struct RouteParams {
     float scale;
 };
 // The few-token layer's list of the expert matrices to stream: plan[0] blocks
-// of at most `cap` rows of one expert, block i at plan[4 + 4i]: expert, first
-// row, rows.
+// of at most `cap` <= 16 rows of one expert, from plan + 4.
+struct FewBlock {
+    int expert, row0, rows, pad;
+    uint8_t token[16];
+};
 struct RoutePlan {
     int *plan;
     int cap;
@@ -105,15 +108,13 @@ struct FewParams {
     const uint8_t *w2, *w2s;  // [E, H, I]
     uint16_t *out;            // [T, H] bf16
     RouteParams route;        // its lens, row_of and token_of lie in the workspace
-    int *plan;                // workspace, 4 + 4 blocks ints
+    int *plan;                // workspace: 4 ints and T k blocks at most
     uint16_t *h;              // workspace [T k, I] bf16
     float *y;                 // workspace [T k, H]
     int T, E, H, I, k;
     int weights;              // FewWeights
     float swiglu_limit;
 };
-// Most blocks the plan can hold.
-int few_max_blocks(int T, int E, int k);
 hipError_t launch_few_tokens(const FewParams &p, hipStream_t s);
 
 }  // namespace ptgg

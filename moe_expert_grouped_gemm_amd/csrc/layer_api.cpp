@@ -68,7 +68,7 @@ FewWs few_ws(int64_t T, int64_t E, int64_t H, int64_t I, int64_t k)
     w.row_of = w.lens + round256(E * 8);
     w.token_of = w.row_of + round256(T * k * 4);
     w.plan = w.token_of + round256(T * k * 4);
-    w.h = w.plan + round256(16 + 16 * T * k);
+    w.h = w.plan + round256(16 + (int64_t)sizeof(FewBlock) * T * k);
     w.y = w.h + round256(T * k * I * 2);
     w.total = w.y + round256(T * k * H * 4);
     return w;

@@ -105,9 +105,19 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteParams p, int
         if (tid == 0) plan.plan[0] = blocks;
         for (int e = tid; e < p.E; e += kRouteThreads) {
             const int first = s_count[e], end = e + 1 < p.E ? s_count[e + 1] : total;
-            int *b = plan.plan + 4 + 4 * s_blocks[e];
-            for (int r = first; r < end; r += plan.cap, b += 4)
-                *(intx4 *)b = intx4{e, r, min(plan.cap, end - r), 0};
+            FewBlock *b = (FewBlock *)(plan.plan + 4) + s_blocks[e];
+            uint64_t left = s_mask[e];
+            for (int r = first; r < end; r += plan.cap, ++b) {
+                const int n = min(plan.cap, end - r);
+                FewBlock v = {e, r, n, 0, {}};
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (i < n) {
+                        v.token[i] = (uint8_t)__builtin_ctzll(left);
+                        left &= left - 1;
+                    }
+                *b = v;
+            }
         }
     }
     const int pairs = (int)p.T * p.k;
