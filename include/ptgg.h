@@ -664,7 +664,7 @@ size_t pt_rmsnorm_workspace_size(int64_t rows, int64_t cols);
  * Y[row_of[t, j]].  sum(lens) < T * k where an id is -1: pass group_offs, or M
  * = sum(lens).
  *  workspace    optional for at most 64 tokens, else required:
- *               pt_moe_route_workspace_size(T, E, k) bytes, 4-byte aligned
+ *               pt_moe_route_workspace_size(T, E, k) bytes, 16-byte aligned
  *               (word 0 takes the error bits)
  *  Requirements: 1 <= k <= E, E <= PT_MAX_GROUPS, k <= PT_MAX_TOPK, T <= 2^23;
  *  logits 16-byte aligned.

@@ -58,6 +58,7 @@ EXPORTS = (
 )
 
 _lib = None
+_gpu_seen = False
 
 
 class PtggError(RuntimeError):
@@ -72,9 +73,11 @@ def lib_path() -> str:
 
 def load(require_gpu: bool = True):
     """Load libptgg.so (building it first only if it has not been built)."""
-    global _lib
-    if require_gpu and not torch.cuda.is_available():
-        raise RuntimeError("moe_expert_grouped_gemm_amd needs a gfx950 GPU; none is visible")
+    global _lib, _gpu_seen
+    if require_gpu and not _gpu_seen:
+        if not torch.cuda.is_available():
+            raise RuntimeError("moe_expert_grouped_gemm_amd needs a gfx950 GPU; none is visible")
+        _gpu_seen = True
     if _lib is not None:
         return _lib
     if not os.path.exists(_build.LIB):
@@ -166,7 +169,8 @@ def _nbytes(t):
 
 def _stream(stream):
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # the handle alone: building a torch.cuda.Stream for it costs as much as a kernel launch
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

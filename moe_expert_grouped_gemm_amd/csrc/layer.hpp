@@ -61,7 +61,7 @@ struct RouteParams {
     int64_t *lens;            // [E]
     int32_t *row_of;          // [T, k]
     int32_t *token_of;        // [T * k]
-    uint16_t *counts;         // workspace: [parts][E] tokens of each part that chose an expert
+    uint16_t *counts;         // workspace: [parts][route_pitch(E)] tokens of each part that chose an expert
     uint32_t *err;
     int64_t T;
     int E, k;
@@ -81,6 +81,8 @@ struct RoutePlan {
     int cap;
 };
 int route_parts(int64_t T);
+// Experts in a row of the counts, which are read 8 at a time.
+__host__ __device__ constexpr int route_pitch(int E) { return (E + 7) & ~7; }
 hipError_t launch_moe_route(const RouteParams &p, hipStream_t s);
 // At most kRouteChunk tokens; also writes the plan.
 hipError_t launch_moe_route_plan(const RouteParams &p, const RoutePlan &plan, hipStream_t s);

@@ -55,7 +55,7 @@ int check_choice(int64_t T, int64_t E, int64_t k)
     return PT_OK;
 }
 
-int64_t route_bytes(int64_t T, int64_t E) { return kWsHead + (T > kRouteChunk ? round256(route_parts(T) * E * 2) : 0); }
+int64_t route_bytes(int64_t T, int64_t E) { return kWsHead + (T > kRouteChunk ? round256((int64_t)route_parts(T) * route_pitch((int)E) * 2) : 0); }
 
 // The few-token layer's workspace, in bytes from its start.
 struct FewWs {
@@ -169,7 +169,7 @@ int pt_moe_route(const void *logits, const float *bias, int32_t *topk_ids, float
     if (bias && gate != PT_GATE_SIGMOID) return PT_ERR_INVALID_ARG;
     if (!lens || (T > 0 && (!logits || !topk_ids || !topk_weights || !row_of || !token_of))) return PT_ERR_INVALID_ARG;
     if (!aligned(logits, 16) || !aligned(bias, 4) || !aligned(topk_ids, 4) || !aligned(topk_weights, 4) ||
-        !aligned(lens, 8) || !aligned(row_of, 4) || !aligned(token_of, 4) || !aligned(workspace, 4))
+        !aligned(lens, 8) || !aligned(row_of, 4) || !aligned(token_of, 4) || !aligned(workspace, 16))
         return PT_ERR_MISALIGNED;
     if (T > kRouteChunk && (!workspace || workspace_bytes < (size_t)route_bytes(T, E))) return PT_ERR_WORKSPACE;
     if (!device_is_gfx950()) return PT_ERR_UNSUPPORTED;

@@ -19,153 +19,236 @@ namespace {
 
 constexpr int kRouteThreads = 512;
 
-// Exclusive scan of n values v[0..n) in LDS by a kRouteThreads workgroup, n <=
-// 1024; returns the total.
-__device__ __forceinline__ int scan_lds(int *v, int n, int *s_wave)
+// Threads of a chunk's workgroup: where a token takes a whole wave, 16 waves
+// have 4 tokens each (8 waves where a lane's experts take more registers).
+__host__ __device__ constexpr int chunk_threads(int lanes, int epl) { return lanes == 64 && epl <= 4 ? 1024 : 512; }
+
+// A chunk's tokens: their experts and weights to memory, the experts also to
+// s_ids and, as bit t of s_mask[expert], the tokens.  s_mask is zero before.
+// Returns whether this thread saw a NaN.
+template <int LANES, int EPL, int NT>
+__device__ __forceinline__ bool choose_chunk(const RouteParams &p, int64_t t0, int n, uint64_t *s_mask, int *s_ids)
 {
-    constexpr int PER = kRouteMaxExperts / kRouteThreads;
-    const int i0 = threadIdx.x * PER;
-    int own[PER], sum = 0;
+    const int tid = threadIdx.x, sub = tid & (LANES - 1);
+    bool any_nan = false;
+    float next[EPL];
+    if (tid / LANES < n) load_logits<EPL>(p.logits, p.bf16, t0 + tid / LANES, p.E, sub * EPL, next);
+    for (int i = tid / LANES; i < n; i += NT / LANES) {       // a whole group of lanes per token
+        float z[EPL];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        own[i] = i0 + i < n ? v[i0 + i] : 0;
-        sum += own[i];
+        for (int j = 0; j < EPL; ++j) z[j] = next[j];
+        if (i + NT / LANES < n) load_logits<EPL>(p.logits, p.bf16, t0 + i + NT / LANES, p.E, sub * EPL, next);
+        int id;
+        float w;
+        bool nan;
+        choose<LANES, EPL>(p, z, id, w, nan);
+        any_nan |= nan;
+        if (sub < p.k) {
+            p.topk_ids[(t0 + i) * p.k + sub] = id;
+            p.topk_weights[(t0 + i) * p.k + sub] = w;
+            s_ids[i * p.k + sub] = id;
+            if (id >= 0) atomicOr((unsigned long long *)&s_mask[id], 1ull << i);
+        }
     }
-    int total;
-    int at = block_exclusive_scan<kRouteThreads>(sum, s_wave, &total);
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        if (i0 + i < n) v[i0 + i] = at;
-        at += own[i];
-    }
-    __syncthreads();
-    return total;
+    return any_nan;
 }
 
-// One part: chunks of 64 tokens in a row.  ONE: the only part, which finishes
-// the order itself; otherwise row_of receives ranks within the part and
-// counts the part's totals.
-template <int LANES, int EPL, bool ONE>
-__global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteParams p, int chunks_per_part, RoutePlan plan)
+// Exclusive prefix over the workgroup of one value a thread; s_wave: a word per
+// wave.  The caller's barriers separate two calls.
+template <int NT>
+__device__ __forceinline__ int scan_threads(int v, int *s_wave, int *total)
 {
-    constexpr int GROUPS = kRouteThreads / LANES;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    int x = v;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int y = __shfl_up(x, d, 64);
+        if (lane >= d) x += y;
+    }
+    if (lane == 63) s_wave[wave] = x;
+    __syncthreads();
+    int before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < NT / 64; ++w) {
+        const int s = s_wave[w];
+        before += w < wave ? s : 0;
+        all += s;
+    }
+    *total = all;
+    return before + x - v;
+}
+
+// At most 64 tokens: one workgroup chooses, counts and orders.
+template <int LANES, int EPL>
+__global__ __launch_bounds__(chunk_threads(LANES, EPL)) void route_one_kernel(RouteParams p, RoutePlan plan)
+{
+    constexpr int NT = chunk_threads(LANES, EPL), PER = kRouteMaxExperts / NT;
     __shared__ uint64_t s_mask[kRouteMaxExperts];
-    __shared__ int s_count[kRouteMaxExperts];      // tokens of earlier chunks; with ONE, finally the first rows
+    __shared__ int s_first[kRouteMaxExperts];      // each expert's first row
     __shared__ int s_ids[kRouteChunk * kRouteMaxTopk];
-    __shared__ int s_wave[kRouteThreads / 64];
-    const int tid = threadIdx.x, sub = tid & (LANES - 1);
+    __shared__ int s_wave[NT / 64];
+    const int tid = threadIdx.x;
+    for (int e = tid; e < p.E; e += NT) s_mask[e] = 0;
+    __syncthreads();
+    if (choose_chunk<LANES, EPL, NT>(p, 0, (int)p.T, s_mask, s_ids) && p.err) atomicOr(p.err, kErrNanLogit);
+    __syncthreads();
+    // rows in the low half of a word, the plan's blocks in the high one: at most 1024 of either
+    int count[PER], sum = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int e = tid * PER + i, c = e < p.E ? __builtin_popcountll(s_mask[e]) : 0;
+        count[i] = c | (plan.plan ? (c + plan.cap - 1) / plan.cap << 16 : 0);
+        sum += count[i];
+    }
+    int total;
+    int at = scan_threads<NT>(sum, s_wave, &total);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int e = tid * PER + i;
+        if (e < p.E) {
+            const int first = at & 0xFFFF, end = first + (count[i] & 0xFFFF);
+            s_first[e] = first;
+            p.lens[e] = end - first;
+            if (plan.plan) {
+                FewBlock *b = (FewBlock *)(plan.plan + 4) + (at >> 16);
+                uint64_t left = s_mask[e];
+                for (int r = first; r < end; r += plan.cap, ++b) {
+                    const int n = min(plan.cap, end - r);
+                    FewBlock v = {e, r, n, 0, {}};
+#pragma unroll
+                    for (int t = 0; t < 16; ++t)
+                        if (t < n) {
+                            v.token[t] = (uint8_t)__builtin_ctzll(left);
+                            left &= left - 1;
+                        }
+                    *b = v;
+                }
+            }
+        }
+        at += count[i];
+    }
+    if (plan.plan && tid == 0) plan.plan[0] = total >> 16;
+    __syncthreads();
+    const int pairs = (int)p.T * p.k;
+    for (int i = tid; i < pairs; i += NT) {
+        const int id = s_ids[i], t = i / p.k;
+        int row = -1;
+        if (id >= 0) {
+            row = s_first[id] + __builtin_popcountll(s_mask[id] & ((1ull << t) - 1));
+            p.token_of[row] = t;
+        }
+        p.row_of[i] = row;
+        if (i >= (total & 0xFFFF)) p.token_of[i] = -1;
+    }
+}
+
+// One part of many tokens: chunks of 64 in a row.  row_of receives the ranks
+// within the part, counts its totals.
+template <int LANES, int EPL>
+__global__ __launch_bounds__(chunk_threads(LANES, EPL)) void route_kernel(RouteParams p, int chunks_per_part)
+{
+    constexpr int NT = chunk_threads(LANES, EPL);
+    __shared__ uint64_t s_mask[kRouteMaxExperts];
+    __shared__ int s_count[kRouteMaxExperts];      // tokens of earlier chunks
+    __shared__ int s_ids[kRouteChunk * kRouteMaxTopk];
+    const int tid = threadIdx.x;
     const int64_t t_first = (int64_t)blockIdx.x * chunks_per_part * kRouteChunk;
     const int64_t t_last = min(p.T, t_first + (int64_t)chunks_per_part * kRouteChunk);
-    for (int e = tid; e < p.E; e += kRouteThreads) s_count[e] = 0;
+    for (int e = tid; e < p.E; e += NT) s_count[e] = 0, s_mask[e] = 0;
+    __syncthreads();
     bool any_nan = false;
     for (int64_t t0 = t_first; t0 < t_last; t0 += kRouteChunk) {
         const int n = (int)min((int64_t)kRouteChunk, t_last - t0);
-        for (int e = tid; e < p.E; e += kRouteThreads) s_mask[e] = 0;
+        any_nan |= choose_chunk<LANES, EPL, NT>(p, t0, n, s_mask, s_ids);
         __syncthreads();
-        for (int i = tid / LANES; i < n; i += GROUPS) {       // a whole group of lanes per token
-            float z[EPL];
-            load_logits<EPL>(p.logits, p.bf16, t0 + i, p.E, sub * EPL, z);
-            int id;
-            float w;
-            bool nan;
-            choose<LANES, EPL>(p, z, id, w, nan);
-            any_nan |= nan;
-            if (sub < p.k) {
-                p.topk_ids[(t0 + i) * p.k + sub] = id;
-                p.topk_weights[(t0 + i) * p.k + sub] = w;
-                s_ids[i * p.k + sub] = id;
-                if (id >= 0) atomicOr((unsigned long long *)&s_mask[id], 1ull << i);
-            }
-        }
-        __syncthreads();
-        for (int i = tid; i < n * p.k; i += kRouteThreads) {
+        for (int i = tid; i < n * p.k; i += NT) {
             const int id = s_ids[i], t = i / p.k;
-            const int rank = id < 0 ? -1 : s_count[id] + __builtin_popcountll(s_mask[id] & ((1ull << t) - 1));
-            if (ONE) s_ids[i] = rank;                          // one part of one chunk
-            else p.row_of[t0 * p.k + i] = rank;
+            p.row_of[t0 * p.k + i] =
+                id < 0 ? -1 : s_count[id] + __builtin_popcountll(s_mask[id] & ((1ull << t) - 1));
         }
         __syncthreads();
-        for (int e = tid; e < p.E; e += kRouteThreads) s_count[e] += __builtin_popcountll(s_mask[e]);
+        for (int e = tid; e < p.E; e += NT) {
+            s_count[e] += __builtin_popcountll(s_mask[e]);
+            s_mask[e] = 0;
+        }
         __syncthreads();
     }
     if (any_nan && p.err) atomicOr(p.err, kErrNanLogit);
-    if (!ONE) {
-        for (int e = tid; e < p.E; e += kRouteThreads) p.counts[(int64_t)blockIdx.x * p.E + e] = (uint16_t)s_count[e];
-        return;
-    }
-    __shared__ int s_blocks[kRouteMaxExperts];
-    for (int e = tid; e < p.E; e += kRouteThreads) {
-        p.lens[e] = s_count[e];
-        if (plan.plan) s_blocks[e] = (s_count[e] + plan.cap - 1) / plan.cap;
-    }
-    __syncthreads();
-    const int total = scan_lds(s_count, p.E, s_wave);
-    if (plan.plan) {
-        const int blocks = scan_lds(s_blocks, p.E, s_wave);
-        if (tid == 0) plan.plan[0] = blocks;
-        for (int e = tid; e < p.E; e += kRouteThreads) {
-            const int first = s_count[e], end = e + 1 < p.E ? s_count[e + 1] : total;
-            FewBlock *b = (FewBlock *)(plan.plan + 4) + s_blocks[e];
-            uint64_t left = s_mask[e];
-            for (int r = first; r < end; r += plan.cap, ++b) {
-                const int n = min(plan.cap, end - r);
-                FewBlock v = {e, r, n, 0, {}};
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (i < n) {
-                        v.token[i] = (uint8_t)__builtin_ctzll(left);
-                        left &= left - 1;
-                    }
-                *b = v;
-            }
-        }
-    }
-    const int pairs = (int)p.T * p.k;
-    for (int i = tid; i < pairs; i += kRouteThreads) {
-        const int rank = s_ids[i];
-        int row = -1;
-        if (rank >= 0) {
-            row = s_count[p.topk_ids[i]] + rank;               // written by this workgroup before its barriers
-            p.token_of[row] = i / p.k;
-        }
-        p.row_of[i] = row;
-        if (i >= total) p.token_of[i] = -1;
-    }
+    const int pitch = route_pitch(p.E);
+    for (int e = tid; e < pitch; e += NT)
+        p.counts[(int64_t)blockIdx.x * pitch + e] = e < p.E ? (uint16_t)s_count[e] : (uint16_t)0;
 }
 
 // Second kernel of several parts: the part's first row of each expert is the
-// rows of earlier experts plus those of earlier parts.
+// rows of earlier experts plus those of earlier parts.  Every workgroup reads
+// all counts, 8 experts of a part a load: thread t takes column t / side of
+// them and parts t % side, t % side + side, ....
 __global__ __launch_bounds__(kRouteThreads) void route_rows_kernel(RouteParams p, int parts, int chunks_per_part)
 {
     __shared__ int s_before[kRouteMaxExperts], s_total[kRouteMaxExperts];
     __shared__ int s_wave[kRouteThreads / 64];
     const int tid = threadIdx.x, part = blockIdx.x;
+    const int pitch = route_pitch(p.E), columns = pitch / 8;
     for (int e = tid; e < p.E; e += kRouteThreads) s_before[e] = s_total[e] = 0;
     __syncthreads();
-    // E columns, and as many rows of counts side by side as the workgroup has
-    const int side = max(1, kRouteThreads / p.E);
-    for (int i = tid; i < side * p.E; i += kRouteThreads) {
-        const int e = i % p.E;
-        int before = 0, total = 0;
-        for (int b = i / p.E; b < parts; b += side) {
-            const int c = p.counts[(int64_t)b * p.E + e];
-            total += c;
-            before += b < part ? c : 0;
+    // a power of two, so that a column's threads are lanes of one wave or whole waves
+    const int side = 1 << (31 - __builtin_clz(kRouteThreads / columns));
+    const int column = tid / side, lanes = min(side, 64);
+    uint32_t before[8] = {}, total8[8] = {};
+    if (column < columns) {
+#pragma unroll 4
+        for (int b = tid % side; b < parts; b += side) {
+            const uintx4 v = *(const uintx4 *)(p.counts + (int64_t)b * pitch + column * 8);
+            const uint32_t mask = b < part ? ~0u : 0u;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                total8[2 * i] += v[i] & 0xFFFFu;
+                total8[2 * i + 1] += v[i] >> 16;
+                before[2 * i] += v[i] & 0xFFFFu & mask;
+                before[2 * i + 1] += v[i] >> 16 & mask;
+            }
         }
-        atomicAdd(&s_before[e], before);                       // integers: their order does not show
-        atomicAdd(&s_total[e], total);
+    }
+    for (int d = 1; d < lanes; d <<= 1) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            before[i] += (uint32_t)__shfl_xor((int)before[i], d, 64);
+            total8[i] += (uint32_t)__shfl_xor((int)total8[i], d, 64);
+        }
+    }
+    if (column < columns && tid % lanes == 0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (column * 8 + i < p.E) {
+                atomicAdd(&s_before[column * 8 + i], (int)before[i]);      // integers: their order does not show
+                atomicAdd(&s_total[column * 8 + i], (int)total8[i]);
+            }
     }
     __syncthreads();
-    if (part == 0)
-        for (int e = tid; e < p.E; e += kRouteThreads) p.lens[e] = s_total[e];
+    constexpr int PER = kRouteMaxExperts / kRouteThreads;
+    int count[PER], sum = 0, total;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        count[i] = tid * PER + i < p.E ? s_total[tid * PER + i] : 0;
+        sum += count[i];
+    }
+    int at = scan_threads<kRouteThreads>(sum, s_wave, &total);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int e = tid * PER + i;
+        if (e < p.E) {
+            s_before[e] += at;                                 // now the part's first row of the expert
+            if (part == 0) p.lens[e] = count[i];
+        }
+        at += count[i];
+    }
     __syncthreads();
-    const int total = scan_lds(s_total, p.E, s_wave);
     const int64_t i0 = (int64_t)part * chunks_per_part * kRouteChunk * p.k;
     const int64_t i1 = min(p.T * p.k, i0 + (int64_t)chunks_per_part * kRouteChunk * p.k);
     for (int64_t i = i0 + tid; i < i1; i += kRouteThreads) {
         const int id = p.topk_ids[i];
         if (id >= 0) {
-            const int row = s_total[id] + s_before[id] + p.row_of[i];
+            const int row = s_before[id] + p.row_of[i];
             p.row_of[i] = row;
             p.token_of[row] = (int)(i / p.k);
         }
@@ -195,17 +278,10 @@ __global__ __launch_bounds__(kThreads) void route_bwd_kernel(RouteBwdParams p)
         if (id < 0 || id >= p.E) id = -1;
         else g = p.dweights[t * p.k + sub] * p.scale;
     }
-    // the chosen expert's logit, from the lane that holds it
+    // the chosen expert's logit: the row is on its way to this wave already
     float mine = ninf;
-    for (int j = 0; j < p.k; ++j) {
-        const int e = __shfl(id, ((threadIdx.x & 63) & ~(LANES - 1)) + j, 64);
-        float v = ninf;
-#pragma unroll
-        for (int i = 0; i < EPL; ++i)
-            if (e == e0 + i) v = z[i];
-        v = group_max<LANES>(v);
-        if (sub == j) mine = v;
-    }
+    if (id >= 0)
+        mine = p.bf16 ? bf16_to_f32(((const uint16_t *)p.logits)[t * p.E + id]) : ((const float *)p.logits)[t * p.E + id];
     if (!(mine > ninf)) id = -1, g = 0.0f;
     float dc = 0.0f;                                           // gradient of the chosen logit by this lane's slot
     float m = 0.0f, inv = 0.0f, dot = 0.0f;
@@ -230,9 +306,9 @@ __global__ __launch_bounds__(kThreads) void route_bwd_kernel(RouteBwdParams p)
     } else if (p.renorm) {
         // shares in 64 bits, as the forward takes them
         const double v = id >= 0 ? sigmoid64(mine) : 0.0;
-        const double total = group_sum<LANES>(v);
+        const double total = slots_sum<LANES>(v);
         const double share = total > 0.0 ? v / total : 0.0;
-        const double mean = group_sum<LANES>(share * g);
+        const double mean = slots_sum<LANES>(share * g);
         // v (1 - v) / total = share (1 - v)
         dc = id >= 0 ? (float)(share * sigmoid64(-mine) * (g - mean)) : 0.0f;
     } else if (id >= 0) {
@@ -243,9 +319,8 @@ __global__ __launch_bounds__(kThreads) void route_bwd_kernel(RouteBwdParams p)
     for (int i = 0; i < EPL; ++i)
         d[i] = (!p.sigmoid && !p.renorm && z[i] > ninf) ? -expf(z[i] - m) * inv * dot : 0.0f;
     for (int j = 0; j < p.k; ++j) {
-        const int src = ((threadIdx.x & 63) & ~(LANES - 1)) + j;
-        const int e = __shfl(id, src, 64);
-        const float v = __shfl(dc, src, 64);
+        const int e = (int)group_lane<LANES>((uint32_t)id, j);
+        const float v = bits_f32(group_lane<LANES>(f32_bits(dc), j));
 #pragma unroll
         for (int i = 0; i < EPL; ++i)
             if (e == e0 + i) d[i] += v;
@@ -296,11 +371,10 @@ struct RunRoute {
     void operator()() const
     {
         if (p.T <= kRouteChunk)
-            hipLaunchKernelGGL((route_kernel<LANES, EPL, true>), dim3(1), dim3(kRouteThreads), 0, s, p, 1,
-                               plan);
+            hipLaunchKernelGGL((route_one_kernel<LANES, EPL>), dim3(1), dim3(chunk_threads(LANES, EPL)), 0, s, p, plan);
         else
-            hipLaunchKernelGGL((route_kernel<LANES, EPL, false>), dim3((unsigned)parts), dim3(kRouteThreads), 0, s, p,
-                               chunks, plan);
+            hipLaunchKernelGGL((route_kernel<LANES, EPL>), dim3((unsigned)parts), dim3(chunk_threads(LANES, EPL)), 0, s, p,
+                               chunks);
     }
 };
 

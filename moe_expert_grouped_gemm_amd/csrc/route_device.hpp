@@ -54,34 +54,83 @@ __device__ __forceinline__ uint32_t score_key(float s)
     return u ^ ((u >> 31) ? 0xFFFFFFFFu : 0x80000000u);
 }
 
-// Reductions over LANES lanes (a power of two; every lane of the group active).
-template <int LANES>
-__device__ __forceinline__ float group_sum(float x)
+// One step of a reduction over 2, 4, ... 64 lanes: op(x, its value in the other
+// half of each 2 D lanes), the smaller groups being uniform already.  All on
+// the vector ALU: DPP within 16 lanes, the row swaps above.
+template <int D, class Op>
+__device__ __forceinline__ uint32_t step_u32(uint32_t x, Op op)
 {
-#pragma unroll
-    for (int d = 1; d < LANES; d <<= 1) x += __shfl_xor(x, d, 64);
+    if constexpr (D <= 8) {
+        constexpr int ctrl = D == 1 ? 0xB1 : D == 2 ? 0x4E : D == 4 ? 0x141 : 0x140;
+        return op(x, (uint32_t)__builtin_amdgcn_update_dpp((int)x, (int)x, ctrl, 0xF, 0xF, false));
+    } else if constexpr (D == 16) {
+        const auto r = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+        return op(r[0], r[1]);
+    } else {
+        const auto r = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+        return op(r[0], r[1]);
+    }
+}
+
+// Reductions over LANES lanes (a power of two; every lane of the group
+// active): all lanes get the result, the same bits in each.
+template <int LANES, class Op>
+__device__ __forceinline__ uint32_t group_reduce(uint32_t x, Op op)
+{
+    if constexpr (LANES > 1) x = step_u32<1>(x, op);
+    if constexpr (LANES > 2) x = step_u32<2>(x, op);
+    if constexpr (LANES > 4) x = step_u32<4>(x, op);
+    if constexpr (LANES > 8) x = step_u32<8>(x, op);
+    if constexpr (LANES > 16) x = step_u32<16>(x, op);
+    if constexpr (LANES > 32) x = step_u32<32>(x, op);
     return x;
 }
 template <int LANES>
-__device__ __forceinline__ double group_sum(double x)
+__device__ __forceinline__ float group_sum(float x)
 {
-#pragma unroll
-    for (int d = 1; d < LANES; d <<= 1) x += __shfl_xor(x, d, 64);
+    return bits_f32(group_reduce<LANES>(f32_bits(x), [](uint32_t a, uint32_t b) { return f32_bits(bits_f32(a) + bits_f32(b)); }));
+}
+// x of the group's lane j, in every lane.
+template <int LANES>
+__device__ __forceinline__ uint32_t group_lane(uint32_t x, int j)
+{
+    if constexpr (LANES == 64) return (uint32_t)__builtin_amdgcn_readlane((int)x, j);
+    return (uint32_t)__shfl((int)x, ((threadIdx.x & 63) & ~(LANES - 1)) + j, 64);
+}
+// Over the slots of a token, which lie in the group's first 16 lanes at most
+// and are zero elsewhere; valid in those lanes.
+template <int LANES>
+__device__ __forceinline__ float slots_sum(float x)
+{
+    return group_sum<LANES < 16 ? LANES : 16>(x);
+}
+template <int D>
+__device__ __forceinline__ double add_step(double x)
+{
+    constexpr int ctrl = D == 1 ? 0xB1 : D == 2 ? 0x4E : D == 4 ? 0x141 : 0x140;
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    const uint32_t l = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, ctrl, 0xF, 0xF, false);
+    const uint32_t h = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), ctrl, 0xF, 0xF, false);
+    return x + __builtin_bit_cast(double, (uint64_t)h << 32 | l);
+}
+template <int LANES>
+__device__ __forceinline__ double slots_sum(double x)
+{
+    x = add_step<4>(add_step<2>(add_step<1>(x)));
+    if constexpr (LANES > 8) x = add_step<8>(x);
     return x;
 }
 template <int LANES>
 __device__ __forceinline__ float group_max(float x)
 {
-#pragma unroll
-    for (int d = 1; d < LANES; d <<= 1) x = __builtin_fmaxf(x, __shfl_xor(x, d, 64));
-    return x;
+    return bits_f32(group_reduce<LANES>(f32_bits(x), [](uint32_t a, uint32_t b) {
+        return f32_bits(__builtin_fmaxf(bits_f32(a), bits_f32(b)));
+    }));
 }
 template <int LANES>
 __device__ __forceinline__ uint32_t group_max_u32(uint32_t x)
 {
-#pragma unroll
-    for (int d = 1; d < LANES; d <<= 1) x = max(x, (uint32_t)__shfl_xor((int)x, d, 64));
-    return x;
+    return group_reduce<LANES>(x, [](uint32_t a, uint32_t b) { return max(a, b); });
 }
 
 // The sigmoid in 64 bits: scores that differ by less than fp32 can tell apart
@@ -89,74 +138,149 @@ __device__ __forceinline__ uint32_t group_max_u32(uint32_t x)
 // all lie far below zero would have no shares left.
 __device__ __forceinline__ double sigmoid64(float z) { return 1.0 / (1.0 + exp(-(double)z)); }
 
-// Choose the k experts with the largest scores (ties to the lowest index) and
-// their weights.  Lane j < k of the group returns the j-th expert (-1: none
-// left that can be chosen) and its weight.  nan: a NaN among the scores.
+// The score's inverse for keys that are not 0.
+__device__ __forceinline__ float key_score(uint32_t k) { return bits_f32(k ^ ((k >> 31) ? 0x80000000u : 0xFFFFFFFFu)); }
+
+// What a slot's lane knows of its expert.
+struct Slot {
+    int id;                   // -1: none
+    float logit, bias;
+    uint32_t key;
+};
+
+// The k largest keys of the group, ties to the lowest expert; lane j < k gets
+// the j-th one (id -1 where all the rest are 0).  Taken keys become 0.
 template <int LANES, int EPL>
-__device__ __forceinline__ void choose(const RouteParams &p, const float (&z)[EPL], int &id, float &weight, bool &nan)
+__device__ __forceinline__ Slot take_largest(int k, uint32_t (&key)[EPL], const float (&z)[EPL], const float (&bias)[EPL],
+                                             bool biased)
 {
     const int sub = threadIdx.x & (LANES - 1), e0 = sub * EPL;
-    uint32_t key[EPL];
-    nan = false;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-        float s = z[i];
-        if (p.sigmoid && z[i] > -__builtin_huge_valf()) {
-            const float b = p.bias && e0 + i < p.E ? p.bias[e0 + i] : 0.0f;
-            s = (float)(sigmoid64(z[i]) + (double)b);
-        }
-        nan |= s != s;
-        key[i] = score_key(s);
-    }
-    id = -1;
-    float mine = -__builtin_huge_valf();
-    const uint64_t group = LANES == 64 ? ~0ull : ((1ull << (LANES & 63)) - 1) << ((threadIdx.x & 63) & ~(LANES - 1));
-    for (int j = 0; j < p.k; ++j) {
+    Slot s = {-1, -__builtin_huge_valf(), 0.0f, 0};
+    for (int j = 0; j < k; ++j) {
         uint32_t best = 0;
         int at = 0;
-        float bz = 0.0f;
+        float bz = 0.0f, bb = 0.0f;
 #pragma unroll
         for (int i = 0; i < EPL; ++i)
-            if (key[i] > best) best = key[i], at = i, bz = z[i];
+            if (key[i] > best) best = key[i], at = i, bz = z[i], bb = bias[i];
         const uint32_t top = group_max_u32<LANES>(best);
-        const uint64_t have = __ballot(best == top) & group;
-        const int lane = __builtin_ctzll(have);                    // the group is never empty
-        const int e = __shfl(e0 + at, lane, 64);
-        const float ez = __shfl(bz, lane, 64);
+        const bool have = top != 0 && best == top;
+        int lane;
+        uint32_t e, ez, eb = 0;
+        if constexpr (LANES == 64) {
+            const uint64_t who = __ballot(have);
+            if (!who) break;
+            lane = __builtin_ctzll(who);
+            e = group_lane<64>((uint32_t)(e0 + at), lane);
+            ez = group_lane<64>(f32_bits(bz), lane);
+            if (biased) eb = group_lane<64>(f32_bits(bb), lane);
+        } else {
+            // the lowest lane that has it, by the largest complement; then one owner, and zeros from the others
+            lane = (int)~group_max_u32<LANES>(have ? ~(uint32_t)sub : 0u);
+            const bool owner = have && lane == sub;
+            e = group_max_u32<LANES>(owner ? (uint32_t)(e0 + at) : 0u);
+            ez = group_max_u32<LANES>(owner ? f32_bits(bz) : 0u);
+            if (biased) eb = group_max_u32<LANES>(owner ? f32_bits(bb) : 0u);
+        }
         if (top != 0) {
-            if (sub == j) id = e, mine = ez;
-            if ((int)(threadIdx.x & 63) == lane) {
+            if (sub == j) s = {(int)e, bits_f32(ez), bits_f32(eb), top};
+            if (sub == lane) {
 #pragma unroll
                 for (int i = 0; i < EPL; ++i)
                     if (i == at) key[i] = 0;
             }
         }
     }
-    if (p.sigmoid) {
-        double v = id >= 0 ? sigmoid64(mine) : 0.0;
-        if (p.renorm) {
-            const double total = group_sum<LANES>(v);
-            v = total > 0.0 ? v / total : 0.0;
-        }
-        weight = (float)(v * (double)p.scale);
-    } else {
-        // largest logit first: softmax over the chosen (renorm) or over all
-        float m = mine;
-        if (!p.renorm) {
+    return s;
+}
+
+// Choose the k experts with the largest scores (ties to the lowest index) and
+// their weights.  Lane j < k of the group returns the j-th expert (-1: none
+// left that can be chosen) and its weight.  nan: a NaN among the scores.
+//
+// Sigmoid scores are ordered as 64 bits rounded to 32 give them, which is dear
+// for every expert.  Scores in 32 bits, off by less than half of `margin`, name
+// the candidates; where exactly k of them reach the k-th one's neighbourhood,
+// only those are computed in 64 bits and put in order, else all are.
+template <int LANES, int EPL>
+__device__ __forceinline__ void choose(const RouteParams &p, const float (&z)[EPL], int &id, float &weight, bool &nan)
+{
+    const int sub = threadIdx.x & (LANES - 1), e0 = sub * EPL;
+    const float ninf = -__builtin_huge_valf();
+    uint32_t key[EPL];
+    float bias[EPL];
+    nan = false;
+    if (!p.sigmoid) {
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) m = __builtin_fmaxf(m, z[i]);
+        for (int i = 0; i < EPL; ++i) {
+            nan |= z[i] != z[i];
+            bias[i] = 0.0f;
+            key[i] = score_key(z[i]);
         }
-        m = group_max<LANES>(m);
-        const float e = id >= 0 ? expf(mine - m) : 0.0f;
-        float total = e;
-        if (!p.renorm) {
+        const Slot s = take_largest<LANES, EPL>(p.k, key, z, bias, false);
+        id = s.id;
+        // the largest logit of all is the first slot's
+        const float m = bits_f32(group_lane<LANES>(f32_bits(s.logit), 0));
+        const float e = id >= 0 ? expf(s.logit - m) : 0.0f;
+        float total;
+        if (p.renorm) {
+            total = slots_sum<LANES>(e);
+        } else {
             total = 0.0f;
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) total += z[i] > -__builtin_huge_valf() ? expf(z[i] - m) : 0.0f;
+            for (int i = 0; i < EPL; ++i) total += z[i] > ninf ? expf(z[i] - m) : 0.0f;
+            total = group_sum<LANES>(total);
         }
-        total = group_sum<LANES>(total);
         weight = id >= 0 ? e / total * p.scale : 0.0f;
+        return;
     }
+    float near[EPL];
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) bias[i] = p.bias && e0 + i < p.E ? p.bias[e0 + i] : 0.0f;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+        near[i] = z[i] > ninf ? __builtin_amdgcn_rcpf(1.0f + __expf(-z[i])) + bias[i] : z[i];
+        nan |= near[i] != near[i];
+        key[i] = score_key(near[i]);
+    }
+    Slot s = take_largest<LANES, EPL>(p.k, key, z, bias, true);
+    // a sigmoid is off by less than 2^-22 (|z| v (1 - v) < 1/4 bounds the exponent's rounding, and three more
+    // roundings of 2^-24), the sum with the bias by a rounding
+    const uint32_t kth = group_max_u32<LANES>(sub == p.k - 1 ? s.key : 0u);
+    const float low = key_score(kth), margin = 0x1p-20f * (1.0f + __builtin_fabsf(low));
+    bool close = false;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) close |= kth != 0 && key[i] != 0 && near[i] >= low - margin;
+    double v;
+    if (group_max_u32<LANES>(close ? 1u : 0u)) {               // one that was not taken is near
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+            key[i] = z[i] > ninf ? score_key((float)(sigmoid64(z[i]) + (double)bias[i])) : 0u;
+        s = take_largest<LANES, EPL>(p.k, key, z, bias, false);
+        id = s.id;
+        v = id >= 0 ? sigmoid64(s.logit) : 0.0;
+    } else {
+        // the chosen ones in the order of their exact scores; lanes without one stay where they are, behind
+        v = s.id >= 0 ? sigmoid64(s.logit) : 0.0;
+        const uint32_t exact = s.id >= 0 ? score_key((float)(v + (double)s.bias)) : 0u;
+        int rank = 0;
+        for (int j = 0; j < p.k; ++j) {
+            const uint32_t other = group_lane<LANES>(exact, j);
+            const int oid = (int)group_lane<LANES>((uint32_t)s.id, j);
+            rank += oid >= 0 && (other > exact || (other == exact && oid < s.id)) ? 1 : 0;
+        }
+        const int to = 4 * (((threadIdx.x & 63) & ~(LANES - 1)) + (s.id >= 0 ? rank : sub));
+        const uint64_t u = __builtin_bit_cast(uint64_t, v);
+        id = __builtin_amdgcn_ds_permute(to, s.id);
+        const uint32_t l = (uint32_t)__builtin_amdgcn_ds_permute(to, (int)(uint32_t)u);
+        const uint32_t h = (uint32_t)__builtin_amdgcn_ds_permute(to, (int)(uint32_t)(u >> 32));
+        v = __builtin_bit_cast(double, (uint64_t)h << 32 | l);
+    }
+    if (p.renorm) {
+        const double total = slots_sum<LANES>(v);
+        v = total > 0.0 ? v / total : 0.0;
+    }
+    weight = (float)(v * (double)p.scale);
 }
 
 }  // namespace ptgg
