@@ -18,36 +18,53 @@ namespace {
 
 constexpr int kFewThreads = 512;          // 8 waves share a block's tokens in LDS
 constexpr int kWaves = kFewThreads / 64;
-constexpr int kFewLds = 65536;            // token rows: two workgroups a CU
+constexpr int kFewLds = 80 * 1024;        // two workgroups a CU
 constexpr int kRows = 16;                 // weight rows of a tile
 constexpr int kDepth = 4;                 // units of 2 KB that a wave keeps in flight
 constexpr int kStage = 2;                 // 16-byte pieces of the token rows a thread has in flight
+constexpr int kScalePieces = 3;           // 8-byte pieces of scales a thread moves
+constexpr int kScaleBytes = kFewThreads * 8 * kScalePieces;
 
 // Elements in 16 bytes of a row, and in a unit, the reduction's step: a whole
 // 128-byte line of each of the tile's rows.
 __host__ __device__ constexpr int piece_elems(int wt) { return wt == kFewBf16 ? 8 : wt == kFewMxfp8 ? 16 : 32; }
 __host__ __device__ constexpr int unit_elems(int wt) { return 8 * piece_elems(wt); }
+__host__ __device__ constexpr int units_of(int K, int wt) { return (K + unit_elems(wt) - 1) / unit_elems(wt); }
+__host__ __device__ constexpr int row_bytes(int K, int wt) { return K / piece_elems(wt) * 16; }
 // LDS bytes of one token's row of K values: padded with zeros to whole units,
 // and 16 bytes so that 16 rows start in different banks.
-__host__ __device__ constexpr int x_pitch(int K, int wt)
+__host__ __device__ constexpr int x_pitch(int K, int wt) { return units_of(K, wt) * unit_elems(wt) * 2 + 16; }
+// Scales of a workgroup's kWaves / splits tiles.
+__host__ __device__ constexpr int scale_region(int K, int wt, int splits)
 {
-    return (K + unit_elems(wt) - 1) / unit_elems(wt) * unit_elems(wt) * 2 + 16;
+    return wt == kFewBf16 ? 0 : kWaves / splits * kRows * (K / 32);
 }
-int row_cap(int K, int wt, int T)
-{
-    const int fit = kFewLds / x_pitch(K, wt), most = T < 16 ? T : 16;
-    return fit < most ? fit : most;
-}
-// Waves that share a tile's reduction.  A wave has 8 KB of loads in flight and
-// the card needs some 16 MB for its bandwidth, so the k experts of a single
-// token should keep 2048 waves; a wave's share is a full ring at least.  The
-// number of tokens does not enter: a token's sums do not depend on who shares
-// its call.
-int k_splits(int tiles, int k, int K, int wt)
+
+// How a product is laid over the waves: `splits` waves share a tile's
+// reduction, a workgroup does kWaves / splits tiles (a group).  The k experts
+// of a single token should keep 1280 waves, since a wave has 8 KB of loads in
+// flight and the card needs some 10 MB for its bandwidth; more waves than that
+// only shorten the streams (1 token, 4 experts of 5760 x 2880 bf16: 25.6 us
+// with 1440 waves, 27.6 with 2880; 2880 x 2880: 14.7 us with 1440, 23.6 with
+// 720).  The number of tokens does not enter: a token's sums do not depend on
+// who shares its call.
+struct Layout {
+    int tiles, splits, groups, lds_fixed;
+};
+Layout layout_of(int tiles, int k, int K, int wt)
 {
     int s = 1;
-    while (s < kWaves && (int64_t)tiles * k * s < 2048 && K / unit_elems(wt) >= 2 * s * kDepth) s *= 2;
-    return s;
+    while (s < kWaves && ((int64_t)tiles * k * s < 1280 || scale_region(K, wt, s) > kScaleBytes) &&
+           units_of(K, wt) >= 2 * s)
+        s *= 2;
+    const int fixed = scale_region(K, wt, s) + (s > 1 ? kFewThreads * 16 : 0);   // and the partial sums
+    return {tiles, s, (tiles * s + kWaves - 1) / kWaves, fixed};
+}
+// Rows a block may have for a product's workgroups to hold them.
+int row_cap(const Layout &l, int K, int wt, int T)
+{
+    const int fit = (kFewLds - l.lds_fixed) / x_pitch(K, wt), most = T < 16 ? T : 16;
+    return fit < most ? fit : most;
 }
 
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
@@ -110,102 +127,6 @@ __device__ __forceinline__ void mma_unit(const uintx4 lo, const uintx4 hi, uint3
     mma_piece<WT>(q, WT == kFewMxfp4 ? e >> 8 : e, x + 2 * piece_elems(WT), acc, 1);
 }
 
-// A wave's share of a tile: n units, and in the last split the rows' partial
-// unit.  A ring of kDepth units (and their scale bytes) stays in flight; the
-// scheduling barriers keep each reload right behind the product that frees its
-// registers.  Every load of start() is unconditional and inside its row, so
-// that the wait for the token rows, issued before, leaves them in flight.
-template <int WT>
-struct Stream {
-    static constexpr int EB = WT == kFewMxfp8 ? 4 : 8;              // scale bytes of a row per unit
-    static constexpr int EL = WT == kFewMxfp8 ? 1 : 2;              // and of a lane
-    static constexpr int XB = unit_elems(WT) * 2;                   // bytes of a token per unit
-    const uint8_t *w0, *w1, *s;
-    int n;
-    uintx4 lo[kDepth], hi[kDepth], last_lo, last_hi;
-    uint32_t e[kDepth], last_e;
-
-    static __device__ __forceinline__ uint32_t scale_at(const uint8_t *p)
-    {
-        if constexpr (EL == 1) return *p;
-        uint16_t v;
-        __builtin_memcpy(&v, p, 2);                                 // rows of K/32 bytes start anywhere
-        return v;
-    }
-    __device__ __forceinline__ void load(int i, int unit)
-    {
-        if constexpr (WT != kFewBf16) {
-            e[i] = scale_at(s + unit * EB);
-            __builtin_amdgcn_sched_barrier(0);
-        }
-        lo[i] = __builtin_nontemporal_load((const uintx4 *)(w0 + unit * 128));
-        __builtin_amdgcn_sched_barrier(0);
-        hi[i] = __builtin_nontemporal_load((const uintx4 *)(w1 + unit * 128));
-        __builtin_amdgcn_sched_barrier(0);
-    }
-    // row0: the weight row of lane % 8, row1 = that of lane % 8 + 8; scales:
-    // those of the row of lane % 16, any: the tensor of them
-    __device__ __forceinline__ void start(const uint8_t *row0, const uint8_t *row1, const uint8_t *scales,
-                                          const uint8_t *any, int K, int split, int splits)
-    {
-        const int lane = threadIdx.x & 63, piece = lane >> 3, g = lane >> 4;
-        const int full = K / unit_elems(WT), rem = K % unit_elems(WT);
-        const int bytes = K * 16 / piece_elems(WT);
-        const int first = full * split / splits;
-        n = full * (split + 1) / splits - first;
-        // a row shorter than a unit has no full one: any of its bytes will do
-        const int at = first * 128 + min(piece * 16, bytes - 16);
-        w0 = row0 + at;
-        w1 = row1 + at;
-        s = full ? scales + first * EB + g * EL : any;
-        const int tail = min(full * 128 + piece * 16, bytes - 16);
-        const bool has = split == splits - 1 && piece * piece_elems(WT) < rem;
-        last_lo = *(const uintx4 *)(row0 + tail);
-        last_hi = *(const uintx4 *)(row1 + tail);
-        last_e = 0;
-        if constexpr (WT != kFewBf16) {
-            const int b = full * EB + g * EL, end = K / 32 - 1;
-            last_e = scales[min(b, end)];
-            if (EL == 2) last_e |= (uint32_t)scales[min(b + 1, end)] << 8;
-        }
-        __builtin_amdgcn_sched_barrier(0);
-        // in the ring's order, so that the first turn's waits are those of the others
-#pragma unroll
-        for (int i = 0; i < kDepth; ++i) load(i, max(min(i, n - 1), 0));
-        // pieces past the rows' end are zeros (x is zero there too, and their scales are some block's of
-        // the row), and so is the whole unit for the earlier splits
-        if (!has) last_lo = last_hi = uintx4{0, 0, 0, 0};
-    }
-    // x: LDS row of token lane % 16, from the lane group's elements of the
-    // split's first unit; x_last: from those of the partial unit.  Returns rows
-    // 4 (lane / 16) + 0..3 of token lane % 16.
-    __device__ __forceinline__ floatx4 product(const uint8_t *x, const uint8_t *x_last, bool tail)
-    {
-        floatx4 acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
-        for (; n >= 2 * kDepth; n -= kDepth) {
-#pragma unroll
-            for (int i = 0; i < kDepth; ++i) {
-                mma_unit<WT>(lo[i], hi[i], e[i], x + i * XB, acc);
-                load(i, kDepth + i);
-            }
-            w0 += kDepth * 128, w1 += kDepth * 128, s += kDepth * EB, x += kDepth * XB;
-        }
-        if (n >= kDepth) {
-#pragma unroll
-            for (int i = 0; i < kDepth; ++i) {
-                mma_unit<WT>(lo[i], hi[i], e[i], x + i * XB, acc);
-                if (kDepth + i < n) load(i, kDepth + i);
-            }
-            n -= kDepth, x += kDepth * XB;
-        }
-#pragma unroll
-        for (int i = 0; i < kDepth - 1; ++i)
-            if (i < n) mma_unit<WT>(lo[i], hi[i], e[i], x + i * XB, acc);
-        if (tail) mma_unit<WT>(last_lo, last_hi, last_e, x_last, acc);
-        return acc[0] + acc[1];
-    }
-};
-
 // A block's token rows into LDS, zeros to the end of the last unit: batches of
 // kStage pieces a thread, the last of them issued before and written after the
 // weights' stream is started.
@@ -249,88 +170,190 @@ struct Stage {
     }
 };
 
-// The partial sums of a tile's splits, added in their order by the first.
-__device__ __forceinline__ floatx4 join_splits(uint8_t *lds, floatx4 c, int split, int splits)
+// One expert's matrix as a product's tiles see it.  FC1: a tile is 8 gate rows
+// and the 8 up rows of the same inner values, ordered so that a lane's four
+// sums are two gates and their two ups.  FC2: 16 rows in a row.
+template <int PHASE>
+struct Rows {
+    int rows, inner;                      // of the matrix; gate rows (FC1)
+    // Row of index i < 16 in a tile, from the tile's first, and where it lies
+    // among the scales of a group of `tiles` (the gates', then the ups').
+    __device__ __forceinline__ int row(int i) const
+    {
+        return PHASE == 1 ? ((i & 2) ? inner : 0) + (i >> 2) * 2 + (i & 1) : i;
+    }
+    __device__ __forceinline__ int scale_row(int slot, int i, int tiles) const
+    {
+        return PHASE == 1 ? ((i & 2) ? tiles * 8 : 0) + slot * 8 + (i >> 2) * 2 + (i & 1) : slot * kRows + i;
+    }
+    static constexpr int step = PHASE == 1 ? 8 : kRows;   // rows from tile to tile
+    static constexpr int half = PHASE == 1 ? 4 : 8;       // from row(i) to row(i + 8)
+};
+
+// The products of one block with a group of tiles, one to `splits` waves.  A
+// wave's stream of units is a ring of kDepth of them in flight; the scheduling
+// barriers keep each reload right behind the product that frees its registers.
+// It starts between the loads of the token rows and the wait for them.  The
+// scales of the group lie in LDS: rows of K/32 bytes read a few at a time would
+// ask for as many lines as the weights do.  NT: the rows are whole lines, each
+// of them read once; else half of them are shared by two units, and the second
+// must find them in the caches (2880-byte rows: 87.7 us cached, 94.1 not;
+// 2048-byte rows: 51.6 and 48.5).  store(tile, c): rows 4 (lane / 16) + 0..3 of
+// token lane % 16.
+template <int WT, int PHASE, bool NT, class Row, class Store>
+__device__ __forceinline__ void block_product(uint8_t *lds, const uint8_t *w, const uint8_t *scales, Rows<PHASE> geo,
+                                              const Layout &l, int m, int K, int group, Row token_row, Store store)
 {
-    floatx4 *part = (floatx4 *)lds + threadIdx.x;
+    constexpr int EB = WT == kFewMxfp8 ? 4 : 8, EL = WT == kFewMxfp8 ? 1 : 2;   // scale bytes of a unit, of a lane
+    constexpr int XB = unit_elems(WT) * 2;
+    constexpr bool MX = WT != kFewBf16;
+    const int pitch = x_pitch(K, WT), rb = row_bytes(K, WT), sb = K / 32, units = units_of(K, WT);
+    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4, piece = lane >> 3;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int splits = l.splits, tiles = kWaves / splits, split = wave % splits, slot = wave / splits;
+    const int first = units * split / splits;
+    int n = units * (split + 1) / splits - first;
+    uint8_t *s_part = lds, *s_scale = lds + (splits > 1 ? kFewThreads * 16 : 0);
+    const int region = MX ? tiles * kRows * sb : 0;
+    uint8_t *s_x = s_scale + region;
+
+    Stage st;
+    st.issue(s_x, pitch, m, K, token_row);
+    // the group's scales, 8 bytes a piece (its rows are whole pieces); past the matrix: its last ones
+    uintx2 sv[kScalePieces];
+    if constexpr (MX) {
+        const int run = PHASE == 1 ? region / 2 : region;              // bytes of consecutive rows
+        const int end = (PHASE == 1 ? geo.inner : geo.rows) * sb;
+#pragma unroll
+        for (int i = 0; i < kScalePieces; ++i) {
+            int at = (i * kFewThreads + (int)threadIdx.x) * 8, from = 0;
+            if (PHASE == 1 && at >= run) at -= run, from = end;
+            __builtin_memcpy(&sv[i], scales + from + min(group * run + at, end - 8), 8);
+        }
+    }
+
+    // the stream: a scalar address and the lanes' offsets from it; past the last tile: that one again.  The last
+    // tile of FC2 may have 8 rows only: those twice.
+    const int tile = group * tiles + slot, t = min(tile, l.tiles - 1);
+    const uint8_t *wp = w + (int64_t)t * geo.step * rb + first * 128;
+    const uint32_t off = (uint32_t)geo.row(lane & 7) * rb + piece * 16;
+    const uint32_t off_hi = off + (uint32_t)((PHASE == 2 && t * kRows + 8 >= geo.rows) ? 0 : geo.half * rb);
+    // the last unit may be short: its pieces past the end read the row's last one and count as zeros (the token
+    // rows are zero there too)
+    const int short_by = units * 128 - rb;
+    const bool cut = short_by != 0 && split == splits - 1;
+    const uint32_t back = (uint32_t)max(piece * 16 - (128 - short_by - 16), 0);
+    uintx4 lo[kDepth], hi[kDepth];
+    const auto load = [&](int i, int unit) {                           // unit: from wp, of the n left
+        const uint32_t b = cut && unit == n - 1 ? back : 0;
+        const uintx4 *p = (const uintx4 *)(wp + unit * 128 + (off - b)), *q = (const uintx4 *)(wp + unit * 128 + (off_hi - b));
+        lo[i] = NT ? __builtin_nontemporal_load(p) : *p;
+        __builtin_amdgcn_sched_barrier(0);
+        hi[i] = NT ? __builtin_nontemporal_load(q) : *q;
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < kDepth; ++i) load(i, min(i, n - 1));
+
+    st.finish(s_x, pitch, m);
+    if constexpr (MX) {
+#pragma unroll
+        for (int i = 0; i < kScalePieces; ++i) {
+            const int at = (i * kFewThreads + (int)threadIdx.x) * 8;
+            if (at < region) *(uintx2 *)(s_scale + at) = sv[i];
+        }
+    }
+    __syncthreads();
+
+    const uint8_t *x = s_x + min(r, m - 1) * pitch + g * piece_elems(WT) * 4 + first * XB;
+    const uint8_t *ep = s_scale + geo.scale_row(slot, r, tiles) * sb + first * EB + g * EL;
+    floatx4 acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+    const auto scale = [&](int unit) -> uint32_t {
+        if constexpr (!MX) return 0;
+        if (EL == 1) return ep[unit * EB];
+        uint16_t v;                                                    // rows of K/32 bytes start anywhere
+        __builtin_memcpy(&v, ep + unit * EB, 2);
+        return v;
+    };
+    const auto multiply = [&](int i, int unit, bool last) {
+        uint32_t e = scale(unit);
+        if (last) {
+            if (piece * 16 >= 128 - short_by) lo[i] = hi[i] = uintx4{0, 0, 0, 0};
+            // scales past the row's end are another's or none: zeros times a NaN would not be zeros
+            if constexpr (MX) {
+                const int b = (units - 1) * EB + g * EL;
+                if (b >= sb) e = 0;
+                if (EL == 2 && b + 1 >= sb) e &= 0xFFu;
+            }
+        }
+        mma_unit<WT>(lo[i], hi[i], e, x + unit * XB, acc);
+    };
+    for (; n >= 2 * kDepth; n -= kDepth) {
+#pragma unroll
+        for (int i = 0; i < kDepth; ++i) {
+            multiply(i, i, false);
+            load(i, kDepth + i);
+        }
+        wp += kDepth * 128, x += kDepth * XB, ep += kDepth * EB;
+    }
+    if (n >= kDepth) {
+#pragma unroll
+        for (int i = 0; i < kDepth; ++i) {
+            multiply(i, i, cut && i == n - 1);
+            if (kDepth + i < n) load(i, kDepth + i);
+        }
+        n -= kDepth, x += kDepth * XB, ep += kDepth * EB;
+    }
+#pragma unroll
+    for (int i = 0; i < kDepth - 1; ++i)
+        if (i < n) multiply(i, i, cut && i == n - 1);
+
+    floatx4 c = acc[0] + acc[1];
     if (splits > 1) {
+        floatx4 *part = (floatx4 *)s_part + threadIdx.x;
         if (split) *part = c;
         __syncthreads();
         if (!split)
-            for (int i = 1; i < splits; ++i) c += part[i * 64];
+            for (int j = 1; j < splits; ++j) c += part[j * 64];
     }
-    return c;
+    if (!split && tile < l.tiles && r < m) store(tile, c);
 }
 
-__host__ __device__ constexpr int row_bytes(int K, int wt) { return wt == kFewBf16 ? K * 2 : wt == kFewMxfp8 ? K : K / 2; }
-
-// The product of a tile that both kernels share.  load_row, step: the weight
-// row (counted over all experts) that this lane loads, and from there to its
-// second; row: the one whose products it takes part in; token_row: the block's
-// rows of x or h.
-template <int WT, class Row>
-__device__ __forceinline__ floatx4 block_product(uint8_t *lds, const uint8_t *w, const uint8_t *scales, int64_t load_row,
-                                                 int step, int64_t row, int m, int K, int split, int splits,
-                                                 Row token_row)
-{
-    const int pitch = x_pitch(K, WT), lane = threadIdx.x & 63, g = lane >> 4;
-    const uint8_t *row0 = w + load_row * row_bytes(K, WT);
-    Stage st;
-    Stream<WT> ws;
-    st.issue(lds, pitch, m, K, token_row);
-    ws.start(row0, row0 + (int64_t)step * row_bytes(K, WT), scales + row * (K / 32), scales, K,
-             split, splits);
-    st.finish(lds, pitch, m);
-    __syncthreads();
-    constexpr int XB = unit_elems(WT) * 2;
-    const int full = K / unit_elems(WT);
-    const uint8_t *x = lds + min(lane & 15, m - 1) * pitch + g * piece_elems(WT) * 4;
-    const floatx4 c = ws.product(x + full * split / splits * XB, x + full * XB,
-                                 K % unit_elems(WT) != 0 && split == splits - 1);
-    if (splits > 1) __syncthreads();          // the token rows make room for the partial sums
-    return join_splits(lds, c, split, splits);
-}
-
-// FC1 and SwiGLU: a tile is 8 gate rows and the 8 up rows of the same inner
-// values, ordered so that a lane gets two gates and their two ups.
-template <int WT>
-__global__ __launch_bounds__(kFewThreads, 4) void few_fc1_kernel(FewParams p, int splits)
+template <int WT, bool NT>
+__global__ __launch_bounds__(kFewThreads, 4) void few_fc1_kernel(FewParams p, Layout l)
 {
     extern __shared__ __align__(16) uint8_t lds[];
     const FewBlock *blk = (const FewBlock *)(p.plan + 4) + blockIdx.y;
     const int blocks = p.plan[0], e = blk->expert, row0 = blk->row0, m = blk->rows;
     const uintx4 tokens = *(const uintx4 *)blk->token;
     if ((int)blockIdx.y >= blocks) return;
-    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
-    const int id = (int)blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int split = id % splits, j0 = id / splits * 8;
-    // waves past the last tile repeat it and store nothing
-    const int64_t tile = (int64_t)e * 2 * p.I + min(j0, p.I - 8);
-    const auto row = [&](int i) { return tile + ((i & 2) ? p.I : 0) + (i >> 2) * 2 + (i & 1); };
-    const floatx4 c = block_product<WT>(lds, p.w1, p.w1s, row(lane & 7), 4, row(r), m, p.H, split, splits, [&](int i) {
-        return p.x + (int64_t)((tokens[i >> 2] >> (8 * (i & 3))) & 0xFFu) * p.H;
-    });
-    if (j0 < p.I && !split && r < m)
-        *(bf16x2_t *)(p.h + (int64_t)(row0 + r) * p.I + j0 + 2 * g) =
-            bf16x2_t{(__bf16)silu_mul(c[0], c[2], p.swiglu_limit), (__bf16)silu_mul(c[1], c[3], p.swiglu_limit)};
+    const int r = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
+    block_product<WT, 1, NT>(
+        lds, p.w1 + (int64_t)e * 2 * p.I * row_bytes(p.H, WT), p.w1s + (int64_t)e * 2 * p.I * (p.H / 32),
+        Rows<1>{2 * p.I, p.I}, l, m, p.H, (int)blockIdx.x,
+        [&](int i) { return p.x + (int64_t)((tokens[i >> 2] >> (8 * (i & 3))) & 0xFFu) * p.H; },
+        [&](int tile, floatx4 c) {
+            *(bf16x2_t *)(p.h + (int64_t)(row0 + r) * p.I + tile * 8 + 2 * g) =
+                bf16x2_t{(__bf16)silu_mul(c[0], c[2], p.swiglu_limit), (__bf16)silu_mul(c[1], c[3], p.swiglu_limit)};
+        });
 }
 
-template <int WT>
-__global__ __launch_bounds__(kFewThreads, 4) void few_fc2_kernel(FewParams p, int splits)
+template <int WT, bool NT>
+__global__ __launch_bounds__(kFewThreads, 4) void few_fc2_kernel(FewParams p, Layout l)
 {
     extern __shared__ __align__(16) uint8_t lds[];
     const FewBlock *blk = (const FewBlock *)(p.plan + 4) + blockIdx.y;
     const int blocks = p.plan[0], e = blk->expert, row0 = blk->row0, m = blk->rows;
     if ((int)blockIdx.y >= blocks) return;
-    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
-    const int id = (int)blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int split = id % splits, n0 = id / splits * kRows;
-    // H % 16 may be 8: the rows past the end repeat the tile's first eight
-    const int64_t tile = (int64_t)e * p.H + min(n0, p.H - 8);
-    const int step = n0 + 8 < p.H ? 8 : 0;
-    const floatx4 c = block_product<WT>(lds, p.w2, p.w2s, tile + (lane & 7), step, tile + (lane & 7) + (r >> 3) * step, m,
-                                        p.I, split, splits, [&](int i) { return p.h + (int64_t)(row0 + i) * p.I; });
-    if (!split && r < m && n0 + 4 * g < p.H) *(floatx4 *)(p.y + (int64_t)(row0 + r) * p.H + n0 + 4 * g) = c;
+    const int r = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
+    block_product<WT, 2, NT>(
+        lds, p.w2 + (int64_t)e * p.H * row_bytes(p.I, WT), p.w2s + (int64_t)e * p.H * (p.I / 32), Rows<2>{p.H, 0}, l, m,
+        p.I, (int)blockIdx.x, [&](int i) { return p.h + (int64_t)(row0 + i) * p.I; },
+        [&](int tile, floatx4 c) {
+            const int n0 = tile * kRows + 4 * g;
+            if (n0 < p.H) *(floatx4 *)(p.y + (int64_t)(row0 + r) * p.H + n0) = c;
+        });
 }
 
 // out[t] = sum over the slots, in their order, of weight times the expert's row.
@@ -366,19 +389,18 @@ __global__ __launch_bounds__(kThreads) void few_sum_kernel(FewParams p)
 }
 
 template <int WT>
-hipError_t launch_products(const FewParams &p, int cap, hipStream_t s)
+hipError_t launch_products(const FewParams &p, const Layout &l1, const Layout &l2, int cap, hipStream_t s)
 {
     // the grid covers the most blocks the routing can give; the rest leave at once
-    const int pairs = p.T * p.k, split = p.E < pairs ? p.E : pairs;
-    int blocks = split + pairs / cap;
-    if (blocks > pairs) blocks = pairs;
-    const int t1 = p.I / 8, t2 = (p.H + kRows - 1) / kRows;
-    const int s1 = k_splits(t1, p.k, p.H, WT), s2 = k_splits(t2, p.k, p.I, WT);
-    const int l1 = cap * x_pitch(p.H, WT), l2 = cap * x_pitch(p.I, WT), room = kFewThreads * 16;
-    hipLaunchKernelGGL(few_fc1_kernel<WT>, dim3((unsigned)((t1 * s1 + kWaves - 1) / kWaves), (unsigned)blocks),
-                       dim3(kFewThreads), l1 > room ? l1 : room, s, p, s1);
-    hipLaunchKernelGGL(few_fc2_kernel<WT>, dim3((unsigned)((t2 * s2 + kWaves - 1) / kWaves), (unsigned)blocks),
-                       dim3(kFewThreads), l2 > room ? l2 : room, s, p, s2);
+    const int pairs = p.T * p.k, most = (p.E < pairs ? p.E : pairs) + pairs / cap;
+    const unsigned blocks = (unsigned)(most < pairs ? most : pairs);
+    const auto whole_lines = [](const void *w, int K) { return ((uintptr_t)w | (uintptr_t)row_bytes(K, WT)) % 128 == 0; };
+    const dim3 g1((unsigned)l1.groups, blocks), g2((unsigned)l2.groups, blocks), b(kFewThreads);
+    const int lds1 = l1.lds_fixed + cap * x_pitch(p.H, WT), lds2 = l2.lds_fixed + cap * x_pitch(p.I, WT);
+    if (whole_lines(p.w1, p.H)) hipLaunchKernelGGL((few_fc1_kernel<WT, true>), g1, b, lds1, s, p, l1);
+    else hipLaunchKernelGGL((few_fc1_kernel<WT, false>), g1, b, lds1, s, p, l1);
+    if (whole_lines(p.w2, p.I)) hipLaunchKernelGGL((few_fc2_kernel<WT, true>), g2, b, lds2, s, p, l2);
+    else hipLaunchKernelGGL((few_fc2_kernel<WT, false>), g2, b, lds2, s, p, l2);
     hipLaunchKernelGGL(few_sum_kernel, dim3((unsigned)((p.H / 4 + kThreads - 1) / kThreads), (unsigned)p.T),
                        dim3(kThreads), 0, s, p);
     return hipGetLastError();
@@ -388,14 +410,16 @@ hipError_t launch_products(const FewParams &p, int cap, hipStream_t s)
 
 hipError_t launch_few_tokens(const FewParams &p, hipStream_t s)
 {
-    const int c1 = row_cap(p.H, p.weights, p.T), c2 = row_cap(p.I, p.weights, p.T);
+    const Layout l1 = layout_of(p.I / 8, p.k, p.H, p.weights);
+    const Layout l2 = layout_of((p.H + kRows - 1) / kRows, p.k, p.I, p.weights);
+    const int c1 = row_cap(l1, p.H, p.weights, p.T), c2 = row_cap(l2, p.I, p.weights, p.T);
     const int cap = c1 < c2 ? c1 : c2;
     hipError_t e = launch_moe_route_plan(p.route, RoutePlan{p.plan, cap}, s);
     if (e != hipSuccess) return e;
     switch (p.weights) {
-    case kFewMxfp8: return launch_products<kFewMxfp8>(p, cap, s);
-    case kFewMxfp4: return launch_products<kFewMxfp4>(p, cap, s);
-    default: return launch_products<kFewBf16>(p, cap, s);
+    case kFewMxfp8: return launch_products<kFewMxfp8>(p, l1, l2, cap, s);
+    case kFewMxfp4: return launch_products<kFewMxfp4>(p, l1, l2, cap, s);
+    default: return launch_products<kFewBf16>(p, l1, l2, cap, s);
     }
 }
 
