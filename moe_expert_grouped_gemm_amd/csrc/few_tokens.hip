@@ -41,21 +41,24 @@ __host__ __device__ constexpr int scale_region(int K, int wt, int splits)
 }
 
 // How a product is laid over the waves: `splits` waves share a tile's
-// reduction, a workgroup does kWaves / splits tiles (a group).  The k experts
-// of a single token should keep 1280 waves, since a wave has 8 KB of loads in
-// flight and the card needs some 10 MB for its bandwidth; more waves than that
-// only shorten the streams (1 token, 4 experts of 5760 x 2880 bf16: 25.6 us
-// with 1440 waves, 27.6 with 2880; 2880 x 2880: 14.7 us with 1440, 23.6 with
-// 720).  The number of tokens does not enter: a token's sums do not depend on
-// who shares its call.
+// reduction, a workgroup does kWaves / splits tiles (a group).  A wave's stream
+// should hold some 16 KB -- twice its ring; longer ones leave too few workgroups
+// to share out evenly, shorter ones are all start and end -- but the k experts
+// of a single token should keep 512 waves.  Measured, FC1 / FC2 in us with 1,
+// 2, 4, 8 waves to a tile: 1 token, 4 experts of 2880 x 2880 bf16 (92 KB tiles):
+// 24.8 / 22.8, 26.8 / 14.4, 22.4 / 15.2, 22.5 / 13.2; 7 tokens, 4096 x 2048
+// MXFP4 (32 and 16 KB): 49 / 27, 47 / 31, 58 / 48, 95 / 88; 64 tokens, the same in
+// bf16 (131 and 65 KB): 551 / 307, 570 / 281, 558 / 291, 604 / 320.  The number of
+// tokens does not enter: a token's sums do not depend on who shares its call.
 struct Layout {
     int tiles, splits, groups, lds_fixed;
 };
 Layout layout_of(int tiles, int k, int K, int wt)
 {
     int s = 1;
-    while (s < kWaves && ((int64_t)tiles * k * s < 1280 || scale_region(K, wt, s) > kScaleBytes) &&
-           units_of(K, wt) >= 2 * s)
+    const int bytes = kRows * row_bytes(K, wt);
+    while (units_of(K, wt) >= 2 * s &&
+           (scale_region(K, wt, s) > kScaleBytes || (s < 4 && (bytes / (2 * s) >= 15 * 1024 || (int64_t)tiles * k * s < 512))))
         s *= 2;
     const int fixed = scale_region(K, wt, s) + (s > 1 ? kFewThreads * 16 : 0);   // and the partial sums
     return {tiles, s, (tiles * s + kWaves - 1) / kWaves, fixed};
@@ -190,29 +193,36 @@ struct Rows {
     static constexpr int half = PHASE == 1 ? 4 : 8;       // from row(i) to row(i + 8)
 };
 
+// How the rows lie.  kShared: lines hold the end of one row and the start of
+// the next, or two units' halves, and the second reader must find them in the
+// caches (2880-byte rows: 87.7 us cached, 94.1 not; 2048-byte rows: 51.6 and
+// 48.5).  kLines: whole lines, each of them read once.  kTurned: also a multiple
+// of 4096 bytes apart, so that waves at the same unit of their rows would meet
+// in a few of the memory's channels: each tile of a workgroup starts at another
+// unit and goes round (8192-byte rows: 614 -> 548 us; the turn costs the
+// others 1%).
+enum Path { kShared = 0, kLines = 1, kTurned = 2 };
+
 // The products of one block with a group of tiles, one to `splits` waves.  A
 // wave's stream of units is a ring of kDepth of them in flight; the scheduling
 // barriers keep each reload right behind the product that frees its registers.
 // It starts between the loads of the token rows and the wait for them.  The
 // scales of the group lie in LDS: rows of K/32 bytes read a few at a time would
-// ask for as many lines as the weights do.  NT: the rows are whole lines, each
-// of them read once; else half of them are shared by two units, and the second
-// must find them in the caches (2880-byte rows: 87.7 us cached, 94.1 not;
-// 2048-byte rows: 51.6 and 48.5).  store(tile, c): rows 4 (lane / 16) + 0..3 of
-// token lane % 16.
-template <int WT, int PHASE, bool NT, class Row, class Store>
+// ask for as many lines as the weights do.  store(tile, c): rows
+// 4 (lane / 16) + 0..3 of token lane % 16.
+template <int WT, int PHASE, int PATH, class Row, class Store>
 __device__ __forceinline__ void block_product(uint8_t *lds, const uint8_t *w, const uint8_t *scales, Rows<PHASE> geo,
                                               const Layout &l, int m, int K, int group, Row token_row, Store store)
 {
     constexpr int EB = WT == kFewMxfp8 ? 4 : 8, EL = WT == kFewMxfp8 ? 1 : 2;   // scale bytes of a unit, of a lane
     constexpr int XB = unit_elems(WT) * 2;
-    constexpr bool MX = WT != kFewBf16;
+    constexpr bool MX = WT != kFewBf16, NT = PATH != kShared;
     const int pitch = x_pitch(K, WT), rb = row_bytes(K, WT), sb = K / 32, units = units_of(K, WT);
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4, piece = lane >> 3;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int splits = l.splits, tiles = kWaves / splits, split = wave % splits, slot = wave / splits;
     const int first = units * split / splits;
-    int n = units * (split + 1) / splits - first;
+    const int n = units * (split + 1) / splits - first, start = PATH == kTurned ? n * slot / tiles : 0;
     uint8_t *s_part = lds, *s_scale = lds + (splits > 1 ? kFewThreads * 16 : 0);
     const int region = MX ? tiles * kRows * sb : 0;
     uint8_t *s_x = s_scale + region;
@@ -244,9 +254,16 @@ __device__ __forceinline__ void block_product(uint8_t *lds, const uint8_t *w, co
     const bool cut = short_by != 0 && split == splits - 1;
     const uint32_t back = (uint32_t)max(piece * 16 - (128 - short_by - 16), 0);
     uintx4 lo[kDepth], hi[kDepth];
-    const auto load = [&](int i, int unit) {                           // unit: from wp, of the n left
-        const uint32_t b = cut && unit == n - 1 ? back : 0;
-        const uintx4 *p = (const uintx4 *)(wp + unit * 128 + (off - b)), *q = (const uintx4 *)(wp + unit * 128 + (off_hi - b));
+    int done = 0;                                                      // units behind wp, x and ep
+    const auto unit_at = [&](int i) {                                  // the i-th from there, counted from them
+        if (PATH != kTurned) return i;
+        const int u = start + done + i;
+        return u >= n ? u - n : u;
+    };
+    const auto load = [&](int i, int unit) {
+        const int u = unit_at(unit);
+        const uint32_t b = cut && u == n - 1 - (PATH == kTurned ? 0 : done) ? back : 0;
+        const uintx4 *p = (const uintx4 *)(wp + u * 128 + (off - b)), *q = (const uintx4 *)(wp + u * 128 + (off_hi - b));
         lo[i] = NT ? __builtin_nontemporal_load(p) : *p;
         __builtin_amdgcn_sched_barrier(0);
         hi[i] = NT ? __builtin_nontemporal_load(q) : *q;
@@ -276,9 +293,10 @@ __device__ __forceinline__ void block_product(uint8_t *lds, const uint8_t *w, co
         __builtin_memcpy(&v, ep + unit * EB, 2);
         return v;
     };
-    const auto multiply = [&](int i, int unit, bool last) {
-        uint32_t e = scale(unit);
-        if (last) {
+    const auto multiply = [&](int i, int unit) {
+        const int u = unit_at(unit);
+        uint32_t e = scale(u);
+        if (cut && u == n - 1 - (PATH == kTurned ? 0 : done)) {
             if (piece * 16 >= 128 - short_by) lo[i] = hi[i] = uintx4{0, 0, 0, 0};
             // scales past the row's end are another's or none: zeros times a NaN would not be zeros
             if constexpr (MX) {
@@ -287,27 +305,30 @@ __device__ __forceinline__ void block_product(uint8_t *lds, const uint8_t *w, co
                 if (EL == 2 && b + 1 >= sb) e &= 0xFFu;
             }
         }
-        mma_unit<WT>(lo[i], hi[i], e, x + unit * XB, acc);
+        mma_unit<WT>(lo[i], hi[i], e, x + u * XB, acc);
     };
-    for (; n >= 2 * kDepth; n -= kDepth) {
+    const auto advance = [&] {
+        done += kDepth;
+        if (PATH != kTurned) wp += kDepth * 128, x += kDepth * XB, ep += kDepth * EB;
+    };
+    for (; n - done >= 2 * kDepth; advance()) {
 #pragma unroll
         for (int i = 0; i < kDepth; ++i) {
-            multiply(i, i, false);
+            multiply(i, i);
             load(i, kDepth + i);
         }
-        wp += kDepth * 128, x += kDepth * XB, ep += kDepth * EB;
     }
-    if (n >= kDepth) {
+    if (n - done >= kDepth) {
 #pragma unroll
         for (int i = 0; i < kDepth; ++i) {
-            multiply(i, i, cut && i == n - 1);
-            if (kDepth + i < n) load(i, kDepth + i);
+            multiply(i, i);
+            if (done + kDepth + i < n) load(i, kDepth + i);
         }
-        n -= kDepth, x += kDepth * XB, ep += kDepth * EB;
+        advance();
     }
 #pragma unroll
     for (int i = 0; i < kDepth - 1; ++i)
-        if (i < n) multiply(i, i, cut && i == n - 1);
+        if (done + i < n) multiply(i, i);
 
     floatx4 c = acc[0] + acc[1];
     if (splits > 1) {
@@ -320,7 +341,7 @@ __device__ __forceinline__ void block_product(uint8_t *lds, const uint8_t *w, co
     if (!split && tile < l.tiles && r < m) store(tile, c);
 }
 
-template <int WT, bool NT>
+template <int WT, int PATH>
 __global__ __launch_bounds__(kFewThreads, 4) void few_fc1_kernel(FewParams p, Layout l)
 {
     extern __shared__ __align__(16) uint8_t lds[];
@@ -329,7 +350,7 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_fc1_kernel(FewParams p, La
     const uintx4 tokens = *(const uintx4 *)blk->token;
     if ((int)blockIdx.y >= blocks) return;
     const int r = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
-    block_product<WT, 1, NT>(
+    block_product<WT, 1, PATH>(
         lds, p.w1 + (int64_t)e * 2 * p.I * row_bytes(p.H, WT), p.w1s + (int64_t)e * 2 * p.I * (p.H / 32),
         Rows<1>{2 * p.I, p.I}, l, m, p.H, (int)blockIdx.x,
         [&](int i) { return p.x + (int64_t)((tokens[i >> 2] >> (8 * (i & 3))) & 0xFFu) * p.H; },
@@ -339,7 +360,7 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_fc1_kernel(FewParams p, La
         });
 }
 
-template <int WT, bool NT>
+template <int WT, int PATH>
 __global__ __launch_bounds__(kFewThreads, 4) void few_fc2_kernel(FewParams p, Layout l)
 {
     extern __shared__ __align__(16) uint8_t lds[];
@@ -347,7 +368,7 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_fc2_kernel(FewParams p, La
     const int blocks = p.plan[0], e = blk->expert, row0 = blk->row0, m = blk->rows;
     if ((int)blockIdx.y >= blocks) return;
     const int r = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
-    block_product<WT, 2, NT>(
+    block_product<WT, 2, PATH>(
         lds, p.w2 + (int64_t)e * p.H * row_bytes(p.I, WT), p.w2s + (int64_t)e * p.H * (p.I / 32), Rows<2>{p.H, 0}, l, m,
         p.I, (int)blockIdx.x, [&](int i) { return p.h + (int64_t)(row0 + i) * p.I; },
         [&](int tile, floatx4 c) {
@@ -388,19 +409,30 @@ __global__ __launch_bounds__(kThreads) void few_sum_kernel(FewParams p)
         bf16x4{(__bf16)sum[0], (__bf16)sum[1], (__bf16)sum[2], (__bf16)sum[3]};
 }
 
+int path_of(const void *w, int rb)
+{
+    if (((uintptr_t)w | (uintptr_t)rb) % 128) return kShared;
+    return rb % 4096 ? kLines : kTurned;
+}
+
 template <int WT>
 hipError_t launch_products(const FewParams &p, const Layout &l1, const Layout &l2, int cap, hipStream_t s)
 {
     // the grid covers the most blocks the routing can give; the rest leave at once
     const int pairs = p.T * p.k, most = (p.E < pairs ? p.E : pairs) + pairs / cap;
     const unsigned blocks = (unsigned)(most < pairs ? most : pairs);
-    const auto whole_lines = [](const void *w, int K) { return ((uintptr_t)w | (uintptr_t)row_bytes(K, WT)) % 128 == 0; };
     const dim3 g1((unsigned)l1.groups, blocks), g2((unsigned)l2.groups, blocks), b(kFewThreads);
     const int lds1 = l1.lds_fixed + cap * x_pitch(p.H, WT), lds2 = l2.lds_fixed + cap * x_pitch(p.I, WT);
-    if (whole_lines(p.w1, p.H)) hipLaunchKernelGGL((few_fc1_kernel<WT, true>), g1, b, lds1, s, p, l1);
-    else hipLaunchKernelGGL((few_fc1_kernel<WT, false>), g1, b, lds1, s, p, l1);
-    if (whole_lines(p.w2, p.I)) hipLaunchKernelGGL((few_fc2_kernel<WT, true>), g2, b, lds2, s, p, l2);
-    else hipLaunchKernelGGL((few_fc2_kernel<WT, false>), g2, b, lds2, s, p, l2);
+    switch (path_of(p.w1, row_bytes(p.H, WT))) {
+    case kTurned: hipLaunchKernelGGL((few_fc1_kernel<WT, kTurned>), g1, b, lds1, s, p, l1); break;
+    case kLines: hipLaunchKernelGGL((few_fc1_kernel<WT, kLines>), g1, b, lds1, s, p, l1); break;
+    default: hipLaunchKernelGGL((few_fc1_kernel<WT, kShared>), g1, b, lds1, s, p, l1);
+    }
+    switch (path_of(p.w2, row_bytes(p.I, WT))) {
+    case kTurned: hipLaunchKernelGGL((few_fc2_kernel<WT, kTurned>), g2, b, lds2, s, p, l2); break;
+    case kLines: hipLaunchKernelGGL((few_fc2_kernel<WT, kLines>), g2, b, lds2, s, p, l2); break;
+    default: hipLaunchKernelGGL((few_fc2_kernel<WT, kShared>), g2, b, lds2, s, p, l2);
+    }
     hipLaunchKernelGGL(few_sum_kernel, dim3((unsigned)((p.H / 4 + kThreads - 1) / kThreads), (unsigned)p.T),
                        dim3(kThreads), 0, s, p);
     return hipGetLastError();
