@@ -667,7 +667,7 @@ size_t pt_rmsnorm_workspace_size(int64_t rows, int64_t cols);
  *               pt_moe_route_workspace_size(T, E, k) bytes, 16-byte aligned
  *               (word 0 takes the error bits)
  *  Requirements: 1 <= k <= E, E <= PT_MAX_GROUPS, k <= PT_MAX_TOPK, T <= 2^23;
- *  logits 16-byte aligned.
+ *  logits and bias 16-byte aligned.
  */
 int pt_moe_route(const void *logits, const float *bias, int32_t *topk_ids, float *topk_weights, int64_t *lens,
                  int32_t *row_of, int32_t *token_of, int64_t T, int64_t E, int64_t k, int logits_dtype, int gate,
@@ -704,7 +704,7 @@ int pt_moe_route_bwd(const void *logits, const int32_t *topk_ids, const float *d
  *  workspace  required: pt_moe_few_tokens_workspace_size(T, E, H, I, k) bytes,
  *        16-byte aligned (word 0 takes the error bits)
  *  Deterministic.  Requirements: H and I % 8 == 0 (bf16) or % 32 == 0 (MX),
- *  H and I <= 16384; x, logits, w1, w2 and out 16-byte aligned; the others as
+ *  H and I <= 16384; x, logits, bias, w1, w2 and out 16-byte aligned; the others as
  *  pt_moe_route.  A weight tensor may exceed 2 GiB.
  */
 int pt_moe_few_tokens(const void *x, const void *logits, const float *bias, const void *w1, const uint8_t *w1_scale,

@@ -168,7 +168,7 @@ int pt_moe_route(const void *logits, const float *bias, int32_t *topk_ids, float
     if (st) return st;
     if (bias && gate != PT_GATE_SIGMOID) return PT_ERR_INVALID_ARG;
     if (!lens || (T > 0 && (!logits || !topk_ids || !topk_weights || !row_of || !token_of))) return PT_ERR_INVALID_ARG;
-    if (!aligned(logits, 16) || !aligned(bias, 4) || !aligned(topk_ids, 4) || !aligned(topk_weights, 4) ||
+    if (!aligned(logits, 16) || !aligned(bias, 16) || !aligned(topk_ids, 4) || !aligned(topk_weights, 4) ||
         !aligned(lens, 8) || !aligned(row_of, 4) || !aligned(token_of, 4) || !aligned(workspace, 16))
         return PT_ERR_MISALIGNED;
     if (T > kRouteChunk && (!workspace || workspace_bytes < (size_t)route_bytes(T, E))) return PT_ERR_WORKSPACE;
@@ -245,7 +245,7 @@ int pt_moe_few_tokens(const void *x, const void *logits, const float *bias, cons
     if (T == 0) return PT_OK;
     if (!x || !logits || !w1 || !w2 || !out || !topk_ids || !topk_weights) return PT_ERR_INVALID_ARG;
     if ((w1_scale != nullptr) != mx || (w2_scale != nullptr) != mx) return PT_ERR_INVALID_ARG;
-    if (!aligned(x, 16) || !aligned(logits, 16) || !aligned(bias, 4) || !aligned(w1, 16) || !aligned(w2, 16) ||
+    if (!aligned(x, 16) || !aligned(logits, 16) || !aligned(bias, 16) || !aligned(w1, 16) || !aligned(w2, 16) ||
         !aligned(out, 16) || !aligned(topk_ids, 4) || !aligned(topk_weights, 4) || !aligned(workspace, 16))
         return PT_ERR_MISALIGNED;
     const FewWs w = few_ws(T, E, H, I, k);

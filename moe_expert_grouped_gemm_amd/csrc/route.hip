@@ -19,9 +19,9 @@ namespace {
 
 constexpr int kRouteThreads = 512;
 
-// Threads of a chunk's workgroup: where a token takes a whole wave, 16 waves
-// have 4 tokens each (8 waves where a lane's experts take more registers).
-__host__ __device__ constexpr int chunk_threads(int lanes, int epl) { return lanes == 64 && epl <= 4 ? 1024 : 512; }
+// Threads of a chunk's workgroup: as many as the registers of a lane's experts
+// allow, since 64 tokens of 16 lanes and more take several turns.
+__host__ __device__ constexpr int chunk_threads(int epl) { return epl <= 8 ? 1024 : 512; }
 
 // A chunk's tokens: their experts and weights to memory, the experts also to
 // s_ids and, as bit t of s_mask[expert], the tokens.  s_mask is zero before.
@@ -31,7 +31,12 @@ __device__ __forceinline__ bool choose_chunk(const RouteParams &p, int64_t t0, i
 {
     const int tid = threadIdx.x, sub = tid & (LANES - 1);
     bool any_nan = false;
-    float next[EPL];
+    float next[EPL], bias[EPL] = {};
+    if (p.bias && tid / LANES < n) {
+        load_logits<EPL>(p.bias, 0, 0, p.E, sub * EPL, bias);  // a row like any other, but its end is 0
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) bias[j] = sub * EPL + j < p.E ? bias[j] : 0.0f;
+    }
     if (tid / LANES < n) load_logits<EPL>(p.logits, p.bf16, t0 + tid / LANES, p.E, sub * EPL, next);
     for (int i = tid / LANES; i < n; i += NT / LANES) {       // a whole group of lanes per token
         float z[EPL];
@@ -41,7 +46,7 @@ __device__ __forceinline__ bool choose_chunk(const RouteParams &p, int64_t t0, i
         int id;
         float w;
         bool nan;
-        choose<LANES, EPL>(p, z, id, w, nan);
+        choose<LANES, EPL>(p, t0 + i, z, bias, id, w, nan);
         any_nan |= nan;
         if (sub < p.k) {
             p.topk_ids[(t0 + i) * p.k + sub] = id;
@@ -80,9 +85,9 @@ __device__ __forceinline__ int scan_threads(int v, int *s_wave, int *total)
 
 // At most 64 tokens: one workgroup chooses, counts and orders.
 template <int LANES, int EPL>
-__global__ __launch_bounds__(chunk_threads(LANES, EPL)) void route_one_kernel(RouteParams p, RoutePlan plan)
+__global__ __launch_bounds__(chunk_threads(EPL)) void route_one_kernel(RouteParams p, RoutePlan plan)
 {
-    constexpr int NT = chunk_threads(LANES, EPL), PER = kRouteMaxExperts / NT;
+    constexpr int NT = chunk_threads(EPL), PER = kRouteMaxExperts / NT;
     __shared__ uint64_t s_mask[kRouteMaxExperts];
     __shared__ int s_first[kRouteMaxExperts];      // each expert's first row
     __shared__ int s_ids[kRouteChunk * kRouteMaxTopk];
@@ -145,9 +150,9 @@ __global__ __launch_bounds__(chunk_threads(LANES, EPL)) void route_one_kernel(Ro
 // One part of many tokens: chunks of 64 in a row.  row_of receives the ranks
 // within the part, counts its totals.
 template <int LANES, int EPL>
-__global__ __launch_bounds__(chunk_threads(LANES, EPL)) void route_kernel(RouteParams p, int chunks_per_part)
+__global__ __launch_bounds__(chunk_threads(EPL)) void route_kernel(RouteParams p, int chunks_per_part)
 {
-    constexpr int NT = chunk_threads(LANES, EPL);
+    constexpr int NT = chunk_threads(EPL);
     __shared__ uint64_t s_mask[kRouteMaxExperts];
     __shared__ int s_count[kRouteMaxExperts];      // tokens of earlier chunks
     __shared__ int s_ids[kRouteChunk * kRouteMaxTopk];
@@ -189,6 +194,11 @@ __global__ __launch_bounds__(kRouteThreads) void route_rows_kernel(RouteParams p
     __shared__ int s_wave[kRouteThreads / 64];
     const int tid = threadIdx.x, part = blockIdx.x;
     const int pitch = route_pitch(p.E), columns = pitch / 8;
+    const int64_t i0 = (int64_t)part * chunks_per_part * kRouteChunk * p.k;
+    const int64_t i1 = min(p.T * p.k, i0 + (int64_t)chunks_per_part * kRouteChunk * p.k);
+    // this thread's first pair is on its way meanwhile
+    const int64_t mine = min(i0 + tid, i1 - 1);
+    const int first_id = p.topk_ids[mine], first_rank = p.row_of[mine];
     for (int e = tid; e < p.E; e += kRouteThreads) s_before[e] = s_total[e] = 0;
     __syncthreads();
     // a power of two, so that a column's threads are lanes of one wave or whole waves
@@ -196,7 +206,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_rows_kernel(RouteParams p
     const int column = tid / side, lanes = min(side, 64);
     uint32_t before[8] = {}, total8[8] = {};
     if (column < columns) {
-#pragma unroll 4
+#pragma unroll 8
         for (int b = tid % side; b < parts; b += side) {
             const uintx4 v = *(const uintx4 *)(p.counts + (int64_t)b * pitch + column * 8);
             const uint32_t mask = b < part ? ~0u : 0u;
@@ -209,12 +219,15 @@ __global__ __launch_bounds__(kRouteThreads) void route_rows_kernel(RouteParams p
             }
         }
     }
-    for (int d = 1; d < lanes; d <<= 1) {
+    const auto add = [](uint32_t a, uint32_t b) { return a + b; };
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            before[i] += (uint32_t)__shfl_xor((int)before[i], d, 64);
-            total8[i] += (uint32_t)__shfl_xor((int)total8[i], d, 64);
-        }
+    for (int i = 0; i < 8; ++i) {
+        if (lanes > 1) before[i] = step_u32<1>(before[i], add), total8[i] = step_u32<1>(total8[i], add);
+        if (lanes > 2) before[i] = step_u32<2>(before[i], add), total8[i] = step_u32<2>(total8[i], add);
+        if (lanes > 4) before[i] = step_u32<4>(before[i], add), total8[i] = step_u32<4>(total8[i], add);
+        if (lanes > 8) before[i] = step_u32<8>(before[i], add), total8[i] = step_u32<8>(total8[i], add);
+        if (lanes > 16) before[i] = step_u32<16>(before[i], add), total8[i] = step_u32<16>(total8[i], add);
+        if (lanes > 32) before[i] = step_u32<32>(before[i], add), total8[i] = step_u32<32>(total8[i], add);
     }
     if (column < columns && tid % lanes == 0) {
 #pragma unroll
@@ -243,12 +256,11 @@ __global__ __launch_bounds__(kRouteThreads) void route_rows_kernel(RouteParams p
         at += count[i];
     }
     __syncthreads();
-    const int64_t i0 = (int64_t)part * chunks_per_part * kRouteChunk * p.k;
-    const int64_t i1 = min(p.T * p.k, i0 + (int64_t)chunks_per_part * kRouteChunk * p.k);
     for (int64_t i = i0 + tid; i < i1; i += kRouteThreads) {
-        const int id = p.topk_ids[i];
+        const bool own = i == i0 + tid;
+        const int id = own ? first_id : p.topk_ids[i];
         if (id >= 0) {
-            const int row = s_before[id] + p.row_of[i];
+            const int row = s_before[id] + (own ? first_rank : p.row_of[i]);
             p.row_of[i] = row;
             p.token_of[row] = (int)(i / p.k);
         }
@@ -349,14 +361,20 @@ __global__ __launch_bounds__(kThreads) void route_bwd_kernel(RouteBwdParams p)
     }
 }
 
-// Lanes per token: four experts a lane, at least as many lanes as slots.
+// Lanes per token, at least as many as slots.  For few tokens four experts a
+// lane: the shortest way through one token.  For many eight: a round of the
+// choice costs a wave about as much whether it holds one token or two (5000
+// tokens, 128 experts, softmax: 17.5 us with 32 lanes each, 8.0 with 16; 16384 of
+// 256, sigmoid: 20.8 with 64, 18.1 with 32).
 template <class Run>
-hipError_t by_width(int E, int k, Run run)
+hipError_t by_width(int64_t T, int E, int k, Run run)
 {
+    const bool few = T <= 16;
     if (E <= 32 && k <= 8) run.template operator()<8, 4>();
-    else if (E <= 64) run.template operator()<16, 4>();
-    else if (E <= 128) run.template operator()<32, 4>();
-    else if (E <= 256) run.template operator()<64, 4>();
+    else if (E <= 64 && (few || k > 8)) run.template operator()<16, 4>();
+    else if (E <= 64) run.template operator()<8, 8>();
+    else if (E <= 128) few ? run.template operator()<32, 4>() : run.template operator()<16, 8>();
+    else if (E <= 256) few ? run.template operator()<64, 4>() : run.template operator()<32, 8>();
     else if (E <= 512) run.template operator()<64, 8>();
     else run.template operator()<64, 16>();
     return hipGetLastError();
@@ -371,9 +389,9 @@ struct RunRoute {
     void operator()() const
     {
         if (p.T <= kRouteChunk)
-            hipLaunchKernelGGL((route_one_kernel<LANES, EPL>), dim3(1), dim3(chunk_threads(LANES, EPL)), 0, s, p, plan);
+            hipLaunchKernelGGL((route_one_kernel<LANES, EPL>), dim3(1), dim3(chunk_threads(EPL)), 0, s, p, plan);
         else
-            hipLaunchKernelGGL((route_kernel<LANES, EPL>), dim3((unsigned)parts), dim3(chunk_threads(LANES, EPL)), 0, s, p,
+            hipLaunchKernelGGL((route_kernel<LANES, EPL>), dim3((unsigned)parts), dim3(chunk_threads(EPL)), 0, s, p,
                                chunks);
     }
 };
@@ -407,7 +425,7 @@ int route_parts(int64_t T)
 hipError_t launch_moe_route(const RouteParams &p, hipStream_t s)
 {
     const int parts = route_parts(p.T), chunks = (int)chunks_per_part(p.T);
-    hipError_t e = by_width(p.E, p.k, RunRoute{p, parts, chunks, RoutePlan{nullptr, 1}, s});
+    hipError_t e = by_width(p.T, p.E, p.k, RunRoute{p, parts, chunks, RoutePlan{nullptr, 1}, s});
     if (e == hipSuccess && p.T > kRouteChunk) {
         hipLaunchKernelGGL(route_rows_kernel, dim3((unsigned)parts), dim3(kRouteThreads), 0, s, p, parts, chunks);
         e = hipGetLastError();
@@ -417,12 +435,12 @@ hipError_t launch_moe_route(const RouteParams &p, hipStream_t s)
 
 hipError_t launch_moe_route_plan(const RouteParams &p, const RoutePlan &plan, hipStream_t s)
 {
-    return by_width(p.E, p.k, RunRoute{p, 1, 1, plan, s});
+    return by_width(p.T, p.E, p.k, RunRoute{p, 1, 1, plan, s});
 }
 
 hipError_t launch_moe_route_bwd(const RouteBwdParams &p, hipStream_t s)
 {
-    return by_width(p.E, p.k, RunRouteBwd{p, s});
+    return by_width(0, p.E, p.k, RunRouteBwd{p, s});      // its loads and stores want whole lines of a token
 }
 
 }  // namespace ptgg

@@ -141,87 +141,85 @@ __device__ __forceinline__ double sigmoid64(float z) { return 1.0 / (1.0 + exp(-
 // The score's inverse for keys that are not 0.
 __device__ __forceinline__ float key_score(uint32_t k) { return bits_f32(k ^ ((k >> 31) ? 0x80000000u : 0xFFFFFFFFu)); }
 
+// One logit, as load_logits gives it.
+__device__ __forceinline__ float logit_at(const void *logits, int bf16, int64_t i)
+{
+    return bf16 ? bf16_to_f32(((const uint16_t *)logits)[i]) : ((const float *)logits)[i];
+}
+
 // What a slot's lane knows of its expert.
 struct Slot {
     int id;                   // -1: none
-    float logit, bias;
     uint32_t key;
 };
 
 // The k largest keys of the group, ties to the lowest expert; lane j < k gets
 // the j-th one (id -1 where all the rest are 0).  Taken keys become 0.
 template <int LANES, int EPL>
-__device__ __forceinline__ Slot take_largest(int k, uint32_t (&key)[EPL], const float (&z)[EPL], const float (&bias)[EPL],
-                                             bool biased)
+__device__ __forceinline__ Slot take_largest(int k, uint32_t (&key)[EPL])
 {
     const int sub = threadIdx.x & (LANES - 1), e0 = sub * EPL;
-    Slot s = {-1, -__builtin_huge_valf(), 0.0f, 0};
+    Slot s = {-1, 0};
     for (int j = 0; j < k; ++j) {
-        uint32_t best = 0;
-        int at = 0;
-        float bz = 0.0f, bb = 0.0f;
+        uint32_t best = key[0];
 #pragma unroll
-        for (int i = 0; i < EPL; ++i)
-            if (key[i] > best) best = key[i], at = i, bz = z[i], bb = bias[i];
+        for (int i = 1; i < EPL; ++i) best = max(best, key[i]);
         const uint32_t top = group_max_u32<LANES>(best);
-        const bool have = top != 0 && best == top;
-        int lane;
-        uint32_t e, ez, eb = 0;
-        if constexpr (LANES == 64) {
-            const uint64_t who = __ballot(have);
-            if (!who) break;
-            lane = __builtin_ctzll(who);
-            e = group_lane<64>((uint32_t)(e0 + at), lane);
-            ez = group_lane<64>(f32_bits(bz), lane);
-            if (biased) eb = group_lane<64>(f32_bits(bb), lane);
-        } else {
-            // the lowest lane that has it, by the largest complement; then one owner, and zeros from the others
-            lane = (int)~group_max_u32<LANES>(have ? ~(uint32_t)sub : 0u);
-            const bool owner = have && lane == sub;
-            e = group_max_u32<LANES>(owner ? (uint32_t)(e0 + at) : 0u);
-            ez = group_max_u32<LANES>(owner ? f32_bits(bz) : 0u);
-            if (biased) eb = group_max_u32<LANES>(owner ? f32_bits(bb) : 0u);
-        }
-        if (top != 0) {
-            if (sub == j) s = {(int)e, bits_f32(ez), bits_f32(eb), top};
-            if (sub == lane) {
+        // the lowest expert that has it: in its lane, then over the lanes
+        int at = 0;
 #pragma unroll
-                for (int i = 0; i < EPL; ++i)
-                    if (i == at) key[i] = 0;
-            }
+        for (int i = EPL - 1; i > 0; --i) {
+            at = key[i] == top ? i : at;
+            // all the comparisons at once would overflow the scalar registers that hold their outcomes
+            if (EPL > 4 && i % 4 == 0) __builtin_amdgcn_sched_barrier(0);
+        }
+        at = key[0] == top ? 0 : at;
+        uint32_t e;
+        if constexpr (LANES == 64) {
+            e = group_lane<64>((uint32_t)(e0 + at), __builtin_ctzll(__ballot(best == top)));   // some lane has it
+        } else {
+            e = ~group_max_u32<LANES>(best == top ? ~(uint32_t)(e0 + at) : 0u);
+        }
+        if (sub == j && top != 0) s = {(int)e, top};
+        // (where nothing is left this clears a 0)
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+            key[i] = (int)e - e0 == i ? 0u : key[i];
+            if (EPL > 4 && i % 4 == 3) __builtin_amdgcn_sched_barrier(0);
         }
     }
     return s;
 }
 
 // Choose the k experts with the largest scores (ties to the lowest index) and
-// their weights.  Lane j < k of the group returns the j-th expert (-1: none
-// left that can be chosen) and its weight.  nan: a NaN among the scores.
+// their weights.  z, bias: the lane's experts' (0 without a bias).  Lane j < k of
+// the group returns the j-th expert (-1: none left that can be chosen) and its
+// weight.  nan: a NaN among the scores.
 //
 // Sigmoid scores are ordered as 64 bits rounded to 32 give them, which is dear
 // for every expert.  Scores in 32 bits, off by less than half of `margin`, name
 // the candidates; where exactly k of them reach the k-th one's neighbourhood,
-// only those are computed in 64 bits and put in order, else all are.
+// only those are computed in 64 bits and put in order, else all that do.
 template <int LANES, int EPL>
-__device__ __forceinline__ void choose(const RouteParams &p, const float (&z)[EPL], int &id, float &weight, bool &nan)
+__device__ __forceinline__ void choose(const RouteParams &p, int64_t t, const float (&z)[EPL], const float (&bias)[EPL],
+                                       int &id, float &weight, bool &nan)
 {
-    const int sub = threadIdx.x & (LANES - 1), e0 = sub * EPL;
+    const int sub = threadIdx.x & (LANES - 1);
     const float ninf = -__builtin_huge_valf();
     uint32_t key[EPL];
-    float bias[EPL];
     nan = false;
     if (!p.sigmoid) {
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
             nan |= z[i] != z[i];
-            bias[i] = 0.0f;
             key[i] = score_key(z[i]);
         }
-        const Slot s = take_largest<LANES, EPL>(p.k, key, z, bias, false);
+        const Slot s = take_largest<LANES, EPL>(p.k, key);
         id = s.id;
+        const float mine = key_score(s.key);
         // the largest logit of all is the first slot's
-        const float m = bits_f32(group_lane<LANES>(f32_bits(s.logit), 0));
-        const float e = id >= 0 ? expf(s.logit - m) : 0.0f;
+        const float m = bits_f32(group_lane<LANES>(f32_bits(mine), 0));
+        const float e = id >= 0 ? expf(mine - m) : 0.0f;
         float total;
         if (p.renorm) {
             total = slots_sum<LANES>(e);
@@ -236,14 +234,12 @@ __device__ __forceinline__ void choose(const RouteParams &p, const float (&z)[EP
     }
     float near[EPL];
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) bias[i] = p.bias && e0 + i < p.E ? p.bias[e0 + i] : 0.0f;
-#pragma unroll
     for (int i = 0; i < EPL; ++i) {
         near[i] = z[i] > ninf ? __builtin_amdgcn_rcpf(1.0f + __expf(-z[i])) + bias[i] : z[i];
         nan |= near[i] != near[i];
         key[i] = score_key(near[i]);
     }
-    Slot s = take_largest<LANES, EPL>(p.k, key, z, bias, true);
+    Slot s = take_largest<LANES, EPL>(p.k, key);
     // a sigmoid is off by less than 2^-22 (|z| v (1 - v) < 1/4 bounds the exponent's rounding, and three more
     // roundings of 2^-24), the sum with the bias by a rounding
     const uint32_t kth = group_max_u32<LANES>(sub == p.k - 1 ? s.key : 0u);
@@ -254,15 +250,21 @@ __device__ __forceinline__ void choose(const RouteParams &p, const float (&z)[EP
     double v;
     if (group_max_u32<LANES>(close ? 1u : 0u)) {               // one that was not taken is near
 #pragma unroll
-        for (int i = 0; i < EPL; ++i)
-            key[i] = z[i] > ninf ? score_key((float)(sigmoid64(z[i]) + (double)bias[i])) : 0u;
-        s = take_largest<LANES, EPL>(p.k, key, z, bias, false);
+        for (int i = 0; i < EPL; ++i) {
+            key[i] = 0;                                        // the others lie lower for certain
+            if (near[i] >= low - margin) key[i] = score_key((float)(sigmoid64(z[i]) + (double)bias[i]));
+        }
+        s = take_largest<LANES, EPL>(p.k, key);
         id = s.id;
-        v = id >= 0 ? sigmoid64(s.logit) : 0.0;
+        v = id >= 0 ? sigmoid64(logit_at(p.logits, p.bf16, t * p.E + id)) : 0.0;
     } else {
         // the chosen ones in the order of their exact scores; lanes without one stay where they are, behind
-        v = s.id >= 0 ? sigmoid64(s.logit) : 0.0;
-        const uint32_t exact = s.id >= 0 ? score_key((float)(v + (double)s.bias)) : 0u;
+        v = 0.0;
+        uint32_t exact = 0;
+        if (s.id >= 0) {
+            v = sigmoid64(logit_at(p.logits, p.bf16, t * p.E + s.id));
+            exact = score_key((float)(v + (double)(p.bias ? p.bias[s.id] : 0.0f)));
+        }
         int rank = 0;
         for (int j = 0; j < p.k; ++j) {
             const uint32_t other = group_lane<LANES>(exact, j);
