@@ -487,8 +487,9 @@ hipError_t launch_rmsnorm_fwd(const NormFwdParams &p, hipStream_t s)
 
 int norm_bwd_parts(int64_t rows)
 {
-    // up to 8 rows one workgroup adds them up itself, which saves a launch
-    if (rows <= 8) return 1;
+    // a few rows one workgroup adds up itself, which saves a launch (4 x 4064 fp32: 6.7 us against 8.8, 8: 11.6 against
+    // 8.9)
+    if (rows <= 5) return 1;
     // each part's row of sums is written and read again, too few parts leave the card idle (517 x 4096 fp32: 13.0 us
     // with 256, 14.0 with 512; 4000 x 2016: 30.0 and 26.6; 16384 x 2880: 81 with 512, 76 with 1024)
     const int64_t most = rows < 1024 ? 256 : rows < 4096 ? 512 : 1024;
