@@ -341,18 +341,38 @@ __device__ __forceinline__ void block_product(uint8_t *lds, const uint8_t *w, co
     if (!split && tile < l.tiles && r < m) store(tile, c);
 }
 
+// Which block and group of tiles a workgroup takes.  An expert's blocks read
+// the same weights: eight groups of them at a time, so that a group's blocks
+// start together and on one XCD (workgroups go round the eight), whose L2 then
+// serves all but the first.
+__device__ __forceinline__ const FewBlock *my_block(const int *plan, int &group)
+{
+    const FewBlock *list = (const FewBlock *)(plan + 4), *b = list + blockIdx.y;
+    const int groups = (int)gridDim.x, of = b->of, first = b->first;
+    group = (int)blockIdx.x;
+    if ((int)blockIdx.y >= plan[0]) return nullptr;
+    if (of > 1) {
+        const int at = ((int)blockIdx.y - first) * groups + group, eight = at / (8 * of) * 8;
+        const int n = min(8, groups - eight), i = at - eight * of;
+        b = list + first + i / n;
+        group = eight + i % n;
+    }
+    return b;
+}
+
 template <int WT, int PATH>
 __global__ __launch_bounds__(kFewThreads, 4) void few_fc1_kernel(FewParams p, Layout l)
 {
     extern __shared__ __align__(16) uint8_t lds[];
-    const FewBlock *blk = (const FewBlock *)(p.plan + 4) + blockIdx.y;
-    const int blocks = p.plan[0], e = blk->expert, row0 = blk->row0, m = blk->rows;
+    int group;
+    const FewBlock *blk = my_block(p.plan, group);
+    if (!blk) return;
+    const int e = blk->expert, row0 = blk->row0, m = blk->rows;
     const uintx4 tokens = *(const uintx4 *)blk->token;
-    if ((int)blockIdx.y >= blocks) return;
     const int r = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
     block_product<WT, 1, PATH>(
         lds, p.w1 + (int64_t)e * 2 * p.I * row_bytes(p.H, WT), p.w1s + (int64_t)e * 2 * p.I * (p.H / 32),
-        Rows<1>{2 * p.I, p.I}, l, m, p.H, (int)blockIdx.x,
+        Rows<1>{2 * p.I, p.I}, l, m, p.H, group,
         [&](int i) { return p.x + (int64_t)((tokens[i >> 2] >> (8 * (i & 3))) & 0xFFu) * p.H; },
         [&](int tile, floatx4 c) {
             *(bf16x2_t *)(p.h + (int64_t)(row0 + r) * p.I + tile * 8 + 2 * g) =
@@ -364,13 +384,14 @@ template <int WT, int PATH>
 __global__ __launch_bounds__(kFewThreads, 4) void few_fc2_kernel(FewParams p, Layout l)
 {
     extern __shared__ __align__(16) uint8_t lds[];
-    const FewBlock *blk = (const FewBlock *)(p.plan + 4) + blockIdx.y;
-    const int blocks = p.plan[0], e = blk->expert, row0 = blk->row0, m = blk->rows;
-    if ((int)blockIdx.y >= blocks) return;
+    int group;
+    const FewBlock *blk = my_block(p.plan, group);
+    if (!blk) return;
+    const int e = blk->expert, row0 = blk->row0, m = blk->rows;
     const int r = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
     block_product<WT, 2, PATH>(
         lds, p.w2 + (int64_t)e * p.H * row_bytes(p.I, WT), p.w2s + (int64_t)e * p.H * (p.I / 32), Rows<2>{p.H, 0}, l, m,
-        p.I, (int)blockIdx.x, [&](int i) { return p.h + (int64_t)(row0 + i) * p.I; },
+        p.I, group, [&](int i) { return p.h + (int64_t)(row0 + i) * p.I; },
         [&](int tile, floatx4 c) {
             const int n0 = tile * kRows + 4 * g;
             if (n0 < p.H) *(floatx4 *)(p.y + (int64_t)(row0 + r) * p.H + n0) = c;

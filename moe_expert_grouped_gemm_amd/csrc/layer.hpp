@@ -71,9 +71,11 @@ struct RouteParams {
     float scale;
 };
 // The few-token layer's list of the expert matrices to stream: plan[0] blocks
-// of at most `cap` <= 16 rows of one expert, from plan + 4.
+// of at most `cap` <= 16 rows of one expert, from plan + 4.  An expert's `of`
+// blocks follow each other from the list's place `first`.
 struct FewBlock {
-    int expert, row0, rows, pad;
+    int expert, row0, rows;
+    uint16_t first, of;
     uint8_t token[16];
 };
 struct RoutePlan {

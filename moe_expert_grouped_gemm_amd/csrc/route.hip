@@ -119,7 +119,7 @@ __global__ __launch_bounds__(chunk_threads(EPL)) void route_one_kernel(RoutePara
                 uint64_t left = s_mask[e];
                 for (int r = first; r < end; r += plan.cap, ++b) {
                     const int n = min(plan.cap, end - r);
-                    FewBlock v = {e, r, n, 0, {}};
+                    FewBlock v = {e, r, n, (uint16_t)(at >> 16), (uint16_t)(count[i] >> 16), {}};
 #pragma unroll
                     for (int t = 0; t < 16; ++t)
                         if (t < n) {
