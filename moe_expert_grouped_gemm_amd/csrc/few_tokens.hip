@@ -10,20 +10,20 @@
 //
 // h = silu(gate) up is rounded to bf16 between the two products, as the grouped
 // GEMM's SwiGLU epilogue does, so decoding and training see the same values.
+#include <type_traits>
+
 #include "route_device.hpp"
 
 namespace ptgg {
 
 namespace {
 
-constexpr int kFewThreads = 512;          // 8 waves share a block's tokens in LDS
-constexpr int kWaves = kFewThreads / 64;
+constexpr int kCuWaves = 16;              // that a CU holds of these kernels, in 4, 2 or 1 workgroups of 4, 8 or 16
 constexpr int kCuLds = 160 * 1024;
 constexpr int kRows = 16;                 // weight rows of a tile
 constexpr int kDepth = 4;                 // units of 2 KB that a wave keeps in flight
 constexpr int kStage = 2;                 // 16-byte pieces of the token rows a thread has in flight
 constexpr int kScalePieces = 3;           // 8-byte pieces of scales a thread moves
-constexpr int kScaleBytes = kFewThreads * 8 * kScalePieces;
 
 // Elements in 16 bytes of a row, and in a unit, the reduction's step: a whole
 // 128-byte line of each of the tile's rows.
@@ -34,14 +34,14 @@ __host__ __device__ constexpr int row_bytes(int K, int wt) { return K / piece_el
 // LDS bytes of one token's row of K values: padded with zeros to whole units,
 // and 16 bytes so that 16 rows start in different banks.
 __host__ __device__ constexpr int x_pitch(int K, int wt) { return units_of(K, wt) * unit_elems(wt) * 2 + 16; }
-// Scales of a workgroup's kWaves / splits tiles.
-__host__ __device__ constexpr int scale_region(int K, int wt, int splits)
+// Scales of a workgroup's waves / splits tiles.
+__host__ __device__ constexpr int scale_region(int K, int wt, int waves, int splits)
 {
-    return wt == kFewBf16 ? 0 : kWaves / splits * kRows * (K / 32);
+    return wt == kFewBf16 ? 0 : waves / splits * kRows * (K / 32);
 }
 
 // How a product is laid over the waves: `splits` waves share a tile's
-// reduction, a workgroup does kWaves / splits tiles (a group).  A wave's stream
+// reduction, a workgroup does waves / splits tiles (a group).  A wave's stream
 // should hold some 16 KB -- twice its ring; longer ones leave too few workgroups
 // to share out evenly, shorter ones are all start and end -- but the k experts
 // of a single token should keep 512 waves.  Measured, FC1 / FC2 in us with 1,
@@ -53,15 +53,17 @@ __host__ __device__ constexpr int scale_region(int K, int wt, int splits)
 struct Layout {
     int tiles, splits, groups, lds_fixed;
 };
-Layout layout_of(int tiles, int k, int K, int wt)
+Layout layout_of(int tiles, int k, int K, int wt, int waves)
 {
     int s = 1;
     const int bytes = kRows * row_bytes(K, wt);
+    const auto scales = [&] { return scale_region(K, wt, kCuWaves, s); };   // of workgroups that fill a CU
     while (units_of(K, wt) >= 2 * s &&
-           (scale_region(K, wt, s) > kScaleBytes || (s < 4 && (bytes / (2 * s) >= 15 * 1024 || (int64_t)tiles * k * s < 512))))
+           (scales() > kCuWaves * 64 * 8 * kScalePieces ||
+            (s < 4 && (bytes / (2 * s) >= 15 * 1024 || (int64_t)tiles * k * s < 512))))
         s *= 2;
-    const int fixed = scale_region(K, wt, s) + (s > 1 ? kFewThreads * 16 : 0);   // and the partial sums
-    return {tiles, s, (tiles * s + kWaves - 1) / kWaves, fixed};
+    const int fixed = scale_region(K, wt, waves, s) + (s > 1 ? waves * 64 * 16 : 0);   // and the partial sums
+    return {tiles, s, (tiles * s + waves - 1) / waves, fixed};
 }
 // Rows a block may have for `per_cu` of a product's workgroups to fit a CU.
 int row_cap(const Layout &l, int K, int wt, int T, int per_cu)
@@ -133,6 +135,7 @@ __device__ __forceinline__ void mma_unit(const uintx4 lo, const uintx4 hi, uint3
 // A block's token rows into LDS, zeros to the end of the last unit: batches of
 // kStage pieces a thread, the last of them issued before and written after the
 // weights' stream is started.
+template <int THREADS>
 struct Stage {
     uintx4 v[kStage];
     int at;
@@ -141,7 +144,7 @@ struct Stage {
     {
 #pragma unroll
         for (int q = 0; q < kStage; ++q) {
-            const int i = min(at + q * kFewThreads + (int)threadIdx.x, all - 1);
+            const int i = min(at + q * THREADS + (int)threadIdx.x, all - 1);
             const int r = i / pieces, c = i - r * pieces;
             v[q] = *(const uintx4 *)(row(r) + min(c * 8, K - 8));
             if (c * 8 >= K) v[q] = uintx4{0, 0, 0, 0};
@@ -152,7 +155,7 @@ struct Stage {
 #pragma unroll
         for (int q = 0; q < kStage; ++q) {
             // past the end: into row 0's padding, which nothing reads (a branch would pull the load behind it)
-            const int i = at + q * kFewThreads + (int)threadIdx.x;
+            const int i = at + q * THREADS + (int)threadIdx.x;
             *(uintx4 *)(lds + (i < all ? i / pieces * pitch + i % pieces * 16 : pitch - 16)) = v[q];
         }
     }
@@ -160,7 +163,7 @@ struct Stage {
     __device__ __forceinline__ void issue(uint8_t *lds, int pitch, int m, int K, Row row)
     {
         const int pieces = (pitch - 16) / 16, all = m * pieces;
-        for (at = 0; at + kStage * kFewThreads < all; at += kStage * kFewThreads) {
+        for (at = 0; at + kStage * THREADS < all; at += kStage * THREADS) {
             load(pieces, all, K, row);
             store(lds, pitch, pieces, all);
         }
@@ -210,24 +213,24 @@ enum Path { kShared = 0, kLines = 1, kTurned = 2 };
 // scales of the group lie in LDS: rows of K/32 bytes read a few at a time would
 // ask for as many lines as the weights do.  store(tile, c): rows
 // 4 (lane / 16) + 0..3 of token lane % 16.
-template <int WT, int PHASE, int PATH, class Row, class Store>
+template <int WT, int PHASE, int PATH, int WAVES, class Row, class Store>
 __device__ __forceinline__ void block_product(uint8_t *lds, const uint8_t *w, const uint8_t *scales, Rows<PHASE> geo,
                                               const Layout &l, int m, int K, int group, Row token_row, Store store)
 {
     constexpr int EB = WT == kFewMxfp8 ? 4 : 8, EL = WT == kFewMxfp8 ? 1 : 2;   // scale bytes of a unit, of a lane
-    constexpr int XB = unit_elems(WT) * 2;
+    constexpr int XB = unit_elems(WT) * 2, THREADS = 64 * WAVES;
     constexpr bool MX = WT != kFewBf16, NT = PATH != kShared;
     const int pitch = x_pitch(K, WT), rb = row_bytes(K, WT), sb = K / 32, units = units_of(K, WT);
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4, piece = lane >> 3;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int splits = l.splits, tiles = kWaves / splits, split = wave % splits, slot = wave / splits;
+    const int splits = l.splits, tiles = WAVES / splits, split = wave % splits, slot = wave / splits;
     const int first = units * split / splits;
     const int n = units * (split + 1) / splits - first, start = PATH == kTurned ? n * slot / tiles : 0;
-    uint8_t *s_part = lds, *s_scale = lds + (splits > 1 ? kFewThreads * 16 : 0);
+    uint8_t *s_part = lds, *s_scale = lds + (splits > 1 ? THREADS * 16 : 0);
     const int region = MX ? tiles * kRows * sb : 0;
     uint8_t *s_x = s_scale + region;
 
-    Stage st;
+    Stage<THREADS> st;
     st.issue(s_x, pitch, m, K, token_row);
     // the group's scales, 8 bytes a piece (its rows are whole pieces); past the matrix: its last ones
     uintx2 sv[kScalePieces];
@@ -236,7 +239,7 @@ __device__ __forceinline__ void block_product(uint8_t *lds, const uint8_t *w, co
         const int end = (PHASE == 1 ? geo.inner : geo.rows) * sb;
 #pragma unroll
         for (int i = 0; i < kScalePieces; ++i) {
-            int at = (i * kFewThreads + (int)threadIdx.x) * 8, from = 0;
+            int at = (i * THREADS + (int)threadIdx.x) * 8, from = 0;
             if (PHASE == 1 && at >= run) at -= run, from = end;
             __builtin_memcpy(&sv[i], scales + from + min(group * run + at, end - 8), 8);
         }
@@ -277,7 +280,7 @@ __device__ __forceinline__ void block_product(uint8_t *lds, const uint8_t *w, co
     if constexpr (MX) {
 #pragma unroll
         for (int i = 0; i < kScalePieces; ++i) {
-            const int at = (i * kFewThreads + (int)threadIdx.x) * 8;
+            const int at = (i * THREADS + (int)threadIdx.x) * 8;
             if (at < region) *(uintx2 *)(s_scale + at) = sv[i];
         }
     }
@@ -341,6 +344,10 @@ __device__ __forceinline__ void block_product(uint8_t *lds, const uint8_t *w, co
     if (!split && tile < l.tiles && r < m) store(tile, c);
 }
 
+// Waves of a SIMD that the registers have to leave room for.  Short rows' LDS lets a third workgroup of 8 waves into a
+// CU, for which 8-bit weights need 80 registers instead of 84 (12 tokens, 60 experts, 736 x 608: 26.8 us to 25.2).
+constexpr int waves_per_simd(int wt, int waves) { return wt == kFewMxfp8 && waves <= 8 ? 6 : 4; }
+
 // Which block and group of tiles a workgroup takes.  An expert's blocks read
 // the same weights: eight groups of them at a time, so that a group's blocks
 // start together and on one XCD (workgroups go round the eight), whose L2 then
@@ -360,8 +367,8 @@ __device__ __forceinline__ const FewBlock *my_block(const int *plan, int &group)
     return b;
 }
 
-template <int WT, int PATH>
-__global__ __launch_bounds__(kFewThreads, 4) void few_fc1_kernel(FewParams p, Layout l)
+template <int WT, int PATH, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, waves_per_simd(WT, WAVES)) void few_fc1_kernel(FewParams p, Layout l)
 {
     extern __shared__ __align__(16) uint8_t lds[];
     int group;
@@ -370,7 +377,7 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_fc1_kernel(FewParams p, La
     const int e = blk->expert, row0 = blk->row0, m = blk->rows;
     const uintx4 tokens = *(const uintx4 *)blk->token;
     const int r = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
-    block_product<WT, 1, PATH>(
+    block_product<WT, 1, PATH, WAVES>(
         lds, p.w1 + (int64_t)e * 2 * p.I * row_bytes(p.H, WT), p.w1s + (int64_t)e * 2 * p.I * (p.H / 32),
         Rows<1>{2 * p.I, p.I}, l, m, p.H, group,
         [&](int i) { return p.x + (int64_t)((tokens[i >> 2] >> (8 * (i & 3))) & 0xFFu) * p.H; },
@@ -380,8 +387,8 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_fc1_kernel(FewParams p, La
         });
 }
 
-template <int WT, int PATH>
-__global__ __launch_bounds__(kFewThreads, 4) void few_fc2_kernel(FewParams p, Layout l)
+template <int WT, int PATH, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, waves_per_simd(WT, WAVES)) void few_fc2_kernel(FewParams p, Layout l)
 {
     extern __shared__ __align__(16) uint8_t lds[];
     int group;
@@ -389,7 +396,7 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_fc2_kernel(FewParams p, La
     if (!blk) return;
     const int e = blk->expert, row0 = blk->row0, m = blk->rows;
     const int r = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
-    block_product<WT, 2, PATH>(
+    block_product<WT, 2, PATH, WAVES>(
         lds, p.w2 + (int64_t)e * p.H * row_bytes(p.I, WT), p.w2s + (int64_t)e * p.H * (p.I / 32), Rows<2>{p.H, 0}, l, m,
         p.I, group, [&](int i) { return p.h + (int64_t)(row0 + i) * p.I; },
         [&](int tile, floatx4 c) {
@@ -436,23 +443,23 @@ int path_of(const void *w, int rb)
     return rb % 4096 ? kLines : kTurned;
 }
 
-template <int WT>
+template <int WT, int WAVES>
 hipError_t launch_products(const FewParams &p, const Layout &l1, const Layout &l2, int cap, hipStream_t s)
 {
     // the grid covers the most blocks the routing can give; the rest leave at once
     const int pairs = p.T * p.k, most = (p.E < pairs ? p.E : pairs) + pairs / cap;
     const unsigned blocks = (unsigned)(most < pairs ? most : pairs);
-    const dim3 g1((unsigned)l1.groups, blocks), g2((unsigned)l2.groups, blocks), b(kFewThreads);
+    const dim3 g1((unsigned)l1.groups, blocks), g2((unsigned)l2.groups, blocks), b(64 * WAVES);
     const int lds1 = l1.lds_fixed + cap * x_pitch(p.H, WT), lds2 = l2.lds_fixed + cap * x_pitch(p.I, WT);
     switch (path_of(p.w1, row_bytes(p.H, WT))) {
-    case kTurned: hipLaunchKernelGGL((few_fc1_kernel<WT, kTurned>), g1, b, lds1, s, p, l1); break;
-    case kLines: hipLaunchKernelGGL((few_fc1_kernel<WT, kLines>), g1, b, lds1, s, p, l1); break;
-    default: hipLaunchKernelGGL((few_fc1_kernel<WT, kShared>), g1, b, lds1, s, p, l1);
+    case kTurned: hipLaunchKernelGGL((few_fc1_kernel<WT, kTurned, WAVES>), g1, b, lds1, s, p, l1); break;
+    case kLines: hipLaunchKernelGGL((few_fc1_kernel<WT, kLines, WAVES>), g1, b, lds1, s, p, l1); break;
+    default: hipLaunchKernelGGL((few_fc1_kernel<WT, kShared, WAVES>), g1, b, lds1, s, p, l1);
     }
     switch (path_of(p.w2, row_bytes(p.I, WT))) {
-    case kTurned: hipLaunchKernelGGL((few_fc2_kernel<WT, kTurned>), g2, b, lds2, s, p, l2); break;
-    case kLines: hipLaunchKernelGGL((few_fc2_kernel<WT, kLines>), g2, b, lds2, s, p, l2); break;
-    default: hipLaunchKernelGGL((few_fc2_kernel<WT, kShared>), g2, b, lds2, s, p, l2);
+    case kTurned: hipLaunchKernelGGL((few_fc2_kernel<WT, kTurned, WAVES>), g2, b, lds2, s, p, l2); break;
+    case kLines: hipLaunchKernelGGL((few_fc2_kernel<WT, kLines, WAVES>), g2, b, lds2, s, p, l2); break;
+    default: hipLaunchKernelGGL((few_fc2_kernel<WT, kShared, WAVES>), g2, b, lds2, s, p, l2);
     }
     hipLaunchKernelGGL(few_sum_kernel, dim3((unsigned)((p.H / 4 + kThreads - 1) / kThreads), (unsigned)p.T),
                        dim3(kThreads), 0, s, p);
@@ -463,24 +470,38 @@ hipError_t launch_products(const FewParams &p, const Layout &l1, const Layout &l
 
 hipError_t launch_few_tokens(const FewParams &p, hipStream_t s)
 {
-    const Layout l1 = layout_of(p.I / 8, p.k, p.H, p.weights);
-    const Layout l2 = layout_of((p.H + kRows - 1) / kRows, p.k, p.I, p.weights);
-    // Two workgroups a CU hide each other's starts; but an expert of more rows than they can hold is read once for
-    // every block of them, so where that would be most experts one workgroup a CU has the room to itself (64
-    // tokens, 8 experts, 6 each, 4032 x 1984 bf16: 263 us against 370; 33 tokens, 32 experts, 4 each, 2880 x 2880 in 8
-    // bits: 153 against 133).  The sums are the same.
-    int cap = 0;
-    for (int per_cu = 2; per_cu >= 1; --per_cu) {
+    // The waves of a workgroup share its tokens' rows and its LDS.  Small workgroups hide each other's starts and end
+    // evenly, which counts where little is read; large ones copy the tokens less often and hold more of them, and an expert
+    // of more rows than they hold is read once for every block of them.  In us with 4, 8 and 16 waves: 1 token, 4 of 32
+    // experts, 2880 x 2880 bf16: 45.4, 47.9, 54.6; 10 tokens, 6 of 60, 1440 x 992 4 bits: 30.2, 32.0, -; 24 tokens, 6 of
+    // 256, 4032 x 1984 4 bits: 216, 210, -; 33 tokens, 4 of 32, 2880 x 2880 8 bits: 155, 133, 145; 64 tokens, 6 of 8, 4032 x
+    // 1984 bf16 (8 waves: one workgroup a CU): -, 236, 194.  The sums are the same.
+    Layout l1, l2;
+    const int pairs = p.T * p.k;
+    const int64_t expert = 2 * (int64_t)p.I * row_bytes(p.H, p.weights) + (int64_t)p.H * row_bytes(p.I, p.weights);
+    int cap = 0, waves = pairs <= p.E && pairs * expert <= (int64_t)1 << 29 ? 4 : 8;
+    for (;; waves *= 2) {
+        l1 = layout_of(p.I / 8, p.k, p.H, p.weights, waves);
+        l2 = layout_of((p.H + kRows - 1) / kRows, p.k, p.I, p.weights, waves);
+        const int per_cu = kCuWaves / waves;
         const int c1 = row_cap(l1, p.H, p.weights, p.T, per_cu), c2 = row_cap(l2, p.I, p.weights, p.T, per_cu);
         cap = c1 < c2 ? c1 : c2;
-        if (cap >= 1 && p.T * p.k <= p.E * cap) break;
+        if (waves == kCuWaves || (cap >= 1 && pairs <= p.E * cap && l1.splits <= waves && l2.splits <= waves)) break;
     }
     hipError_t e = launch_moe_route_plan(p.route, RoutePlan{p.plan, cap}, s);
     if (e != hipSuccess) return e;
+    const auto run = [&](auto wt) {
+        constexpr int WT = decltype(wt)::value;
+        switch (waves) {
+        case 4: return launch_products<WT, 4>(p, l1, l2, cap, s);
+        case 8: return launch_products<WT, 8>(p, l1, l2, cap, s);
+        default: return launch_products<WT, kCuWaves>(p, l1, l2, cap, s);
+        }
+    };
     switch (p.weights) {
-    case kFewMxfp8: return launch_products<kFewMxfp8>(p, l1, l2, cap, s);
-    case kFewMxfp4: return launch_products<kFewMxfp4>(p, l1, l2, cap, s);
-    default: return launch_products<kFewBf16>(p, l1, l2, cap, s);
+    case kFewMxfp8: return run(std::integral_constant<int, kFewMxfp8>{});
+    case kFewMxfp4: return run(std::integral_constant<int, kFewMxfp4>{});
+    default: return run(std::integral_constant<int, kFewBf16>{});
     }
 }
 
