@@ -653,6 +653,8 @@ size_t pt_rmsnorm_workspace_size(int64_t rows, int64_t cols);
  * and every weight times `scale`.  An expert whose logit is -inf or NaN is not
  * chosen (a NaN also sets error bit 4); a token with fewer than k experts left
  * gets id -1 and weight 0 in the slots past them.
+ * A logit of +inf is chosen first; among softmax scores it makes the token's
+ * weights NaN.
  *  logits       [T, E] fp32 or bf16 (logits_dtype PT_FP32 or PT_BF16)
  *  bias         [E] fp32 (PT_GATE_SIGMOID only), or NULL
  *  topk_ids     [T, k] int32, largest score first;  topk_weights [T, k] fp32

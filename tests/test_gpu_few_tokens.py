@@ -138,6 +138,15 @@ def test_widest(dev, kind):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "mxfp8", "mxfp4"])
+@pytest.mark.parametrize("T,E,k", [(1, 4, 2), (40, 2, 2)])
+def test_wide_rows_in_every_workgroup_size(dev, T, E, k, kind):
+    """Few rows per expert and many: the workgroup's waves follow from both, a tile's share of them from the width."""
+    for H, I in ((16384, 32), (32, 16384), (4096, 96)):
+        x, z, _, ops = make(dev, T, E, H, I, kind, T + E + I)
+        check(x, z, None, ops, k, 0, 1, 1.0, kind)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "mxfp8", "mxfp4"])
 def test_clamped_swiglu(dev, kind):
     x, z, _, ops = make(dev, 6, 4, 128, 96, kind, 9)
     check(x * 4, z, None, ops, 2, 0, 1, 1.0, kind, limit=1.5)

@@ -179,6 +179,22 @@ def test_nan_is_never_chosen_and_is_reported(dev, gate):
         assert got["err"] == 16 and got["ids"][3].eq(-1).all()
 
 
+@pytest.mark.parametrize("T", [10, 100])
+def test_plus_infinity_is_chosen_first(dev, T):
+    z, _ = logits(dev, T, 64, 14)
+    z[1, 7] = float("inf")
+    big = z.clone()
+    big[1, 7] = 1e30
+    for gate, renorm in ((0, 0), (0, 1), (1, 0), (1, 1)):
+        got, ref = route(z, None, 4, gate, renorm, 1.0), route(big, None, 4, gate, renorm, 1.0)
+        assert got["err"] == 0 and got["ids"][1, 0] == 7
+        assert all(torch.equal(got[n], ref[n]) for n in ("ids", "lens", "row_of", "token_of"))
+        keep = torch.arange(T, device=dev) != 1
+        assert torch.equal(got["w"][keep], ref["w"][keep])
+        # a softmax with +inf has no value; a sigmoid is 1 there
+        assert got["w"][1].isnan().all() if gate == 0 else torch.equal(got["w"][1], ref["w"][1])
+
+
 def test_scores_that_differ_in_their_last_bit(dev):
     """Sigmoid scores with a bias: the order is that of the fp32-rounded 64-bit scores, near 1 too."""
     g = torch.Generator(device=dev).manual_seed(2)
