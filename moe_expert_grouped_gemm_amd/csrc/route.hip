@@ -9,8 +9,9 @@
 // atomic whose order shows.  With several workgroups (parts of consecutive
 // chunks) a second kernel adds the counts of the parts before.
 //
-// What bounds it: launch and wave-reduction latency; the logits of 16384
-// tokens are 16 MB at most.
+// What bounds it: launch and wave-reduction latency -- a token's choice is a
+// thousand vector instructions of a wave, so it is spread over the CUs; the
+// logits of 16384 tokens are 16 MB at most.
 #include "route_device.hpp"
 
 namespace ptgg {
@@ -18,10 +19,20 @@ namespace ptgg {
 namespace {
 
 constexpr int kRouteThreads = 512;
+constexpr int kOrderThreads = 1024;       // a pair each
 
 // Threads of a chunk's workgroup: as many as the registers of a lane's experts
 // allow, since 64 tokens of 16 lanes and more take several turns.
 __host__ __device__ constexpr int chunk_threads(int epl) { return epl <= 8 ? 1024 : 512; }
+
+// The bias of experts e0 .. e0 + EPL - 1: a row like any other, but its end is 0.
+template <int EPL>
+__device__ __forceinline__ void load_bias(const RouteParams &p, int e0, float (&bias)[EPL])
+{
+    load_logits<EPL>(p.bias, 0, 0, p.E, e0, bias);
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) bias[j] = e0 + j < p.E ? bias[j] : 0.0f;
+}
 
 // A chunk's tokens: their experts and weights to memory, the experts also to
 // s_ids and, as bit t of s_mask[expert], the tokens.  s_mask is zero before.
@@ -32,11 +43,7 @@ __device__ __forceinline__ bool choose_chunk(const RouteParams &p, int64_t t0, i
     const int tid = threadIdx.x, sub = tid & (LANES - 1);
     bool any_nan = false;
     float next[EPL], bias[EPL] = {};
-    if (p.bias && tid / LANES < n) {
-        load_logits<EPL>(p.bias, 0, 0, p.E, sub * EPL, bias);  // a row like any other, but its end is 0
-#pragma unroll
-        for (int j = 0; j < EPL; ++j) bias[j] = sub * EPL + j < p.E ? bias[j] : 0.0f;
-    }
+    if (p.bias && tid / LANES < n) load_bias<EPL>(p, sub * EPL, bias);
     if (tid / LANES < n) load_logits<EPL>(p.logits, p.bf16, t0 + tid / LANES, p.E, sub * EPL, next);
     for (int i = tid / LANES; i < n; i += NT / LANES) {       // a whole group of lanes per token
         float z[EPL];
@@ -83,20 +90,15 @@ __device__ __forceinline__ int scan_threads(int v, int *s_wave, int *total)
     return before + x - v;
 }
 
-// At most 64 tokens: one workgroup chooses, counts and orders.
-template <int LANES, int EPL>
-__global__ __launch_bounds__(chunk_threads(EPL)) void route_one_kernel(RouteParams p, RoutePlan plan)
+// Counts, orders and plans what at most 64 tokens chose, in one workgroup.  Of
+// their choices s_ids has the experts and s_mask, as bit t of s_mask[expert], the
+// tokens.
+template <int NT>
+__device__ __forceinline__ void order_chunk(const RouteParams &p, const RoutePlan &plan, const uint64_t *s_mask,
+                                            const int *s_ids, int *s_first, int *s_wave)
 {
-    constexpr int NT = chunk_threads(EPL), PER = kRouteMaxExperts / NT;
-    __shared__ uint64_t s_mask[kRouteMaxExperts];
-    __shared__ int s_first[kRouteMaxExperts];      // each expert's first row
-    __shared__ int s_ids[kRouteChunk * kRouteMaxTopk];
-    __shared__ int s_wave[NT / 64];
+    constexpr int PER = kRouteMaxExperts / NT;
     const int tid = threadIdx.x;
-    for (int e = tid; e < p.E; e += NT) s_mask[e] = 0;
-    __syncthreads();
-    if (choose_chunk<LANES, EPL, NT>(p, 0, (int)p.T, s_mask, s_ids) && p.err) atomicOr(p.err, kErrNanLogit);
-    __syncthreads();
     // rows in the low half of a word, the plan's blocks in the high one: at most 1024 of either
     int count[PER], sum = 0;
 #pragma unroll
@@ -147,18 +149,71 @@ __global__ __launch_bounds__(chunk_threads(EPL)) void route_one_kernel(RoutePara
     }
 }
 
+// At most 64 tokens: one workgroup chooses, counts and orders.
+template <int LANES, int EPL>
+__global__ __launch_bounds__(chunk_threads(EPL)) void route_one_kernel(RouteParams p, RoutePlan plan)
+{
+    constexpr int NT = chunk_threads(EPL);
+    __shared__ uint64_t s_mask[kRouteMaxExperts];
+    __shared__ int s_first[kRouteMaxExperts];      // each expert's first row
+    __shared__ int s_ids[kRouteChunk * kRouteMaxTopk];
+    __shared__ int s_wave[NT / 64];
+    const int tid = threadIdx.x;
+    for (int e = tid; e < p.E; e += NT) s_mask[e] = 0;
+    __syncthreads();
+    if (choose_chunk<LANES, EPL, NT>(p, 0, (int)p.T, s_mask, s_ids) && p.err) atomicOr(p.err, kErrNanLogit);
+    __syncthreads();
+    order_chunk<NT>(p, plan, s_mask, s_ids, s_first, s_wave);
+}
+
+// The same where one workgroup would take long over the choice: that by a
+// workgroup for every few tokens, then the order by one.
+template <int LANES, int EPL>
+__global__ __launch_bounds__(kThreads) void route_choose_kernel(RouteParams p)
+{
+    const int sub = threadIdx.x & (LANES - 1);
+    const int64_t t = (int64_t)blockIdx.x * (kThreads / LANES) + threadIdx.x / LANES;
+    if (t >= p.T) return;                                      // whole groups
+    float z[EPL], bias[EPL] = {};
+    load_logits<EPL>(p.logits, p.bf16, t, p.E, sub * EPL, z);
+    if (p.bias) load_bias<EPL>(p, sub * EPL, bias);
+    int id;
+    float w;
+    bool nan;
+    choose<LANES, EPL>(p, t, z, bias, id, w, nan);
+    if (nan && p.err) atomicOr(p.err, kErrNanLogit);
+    if (sub < p.k) {
+        p.topk_ids[t * p.k + sub] = id;
+        p.topk_weights[t * p.k + sub] = w;
+    }
+}
+
+__global__ __launch_bounds__(kOrderThreads) void route_order_kernel(RouteParams p, RoutePlan plan)
+{
+    __shared__ uint64_t s_mask[kRouteMaxExperts];
+    __shared__ int s_first[kRouteMaxExperts], s_ids[kRouteChunk * kRouteMaxTopk], s_wave[kOrderThreads / 64];
+    const int tid = threadIdx.x, pairs = (int)p.T * p.k;
+    const int id = tid < pairs ? p.topk_ids[tid] : -1;         // 1024 pairs at most
+    for (int e = tid; e < p.E; e += kOrderThreads) s_mask[e] = 0;
+    __syncthreads();
+    if (tid < pairs) s_ids[tid] = id;
+    if (id >= 0) atomicOr((unsigned long long *)&s_mask[id], 1ull << (tid / p.k));
+    __syncthreads();
+    order_chunk<kOrderThreads>(p, plan, s_mask, s_ids, s_first, s_wave);
+}
+
 // One part of many tokens: chunks of 64 in a row.  row_of receives the ranks
 // within the part, counts its totals.
 template <int LANES, int EPL>
-__global__ __launch_bounds__(chunk_threads(EPL)) void route_kernel(RouteParams p, int chunks_per_part)
+__global__ __launch_bounds__(chunk_threads(EPL)) void route_kernel(RouteParams p, int part_tokens)
 {
     constexpr int NT = chunk_threads(EPL);
     __shared__ uint64_t s_mask[kRouteMaxExperts];
     __shared__ int s_count[kRouteMaxExperts];      // tokens of earlier chunks
     __shared__ int s_ids[kRouteChunk * kRouteMaxTopk];
     const int tid = threadIdx.x;
-    const int64_t t_first = (int64_t)blockIdx.x * chunks_per_part * kRouteChunk;
-    const int64_t t_last = min(p.T, t_first + (int64_t)chunks_per_part * kRouteChunk);
+    const int64_t t_first = (int64_t)blockIdx.x * part_tokens;
+    const int64_t t_last = min(p.T, t_first + part_tokens);
     for (int e = tid; e < p.E; e += NT) s_count[e] = 0, s_mask[e] = 0;
     __syncthreads();
     bool any_nan = false;
@@ -188,14 +243,14 @@ __global__ __launch_bounds__(chunk_threads(EPL)) void route_kernel(RouteParams p
 // rows of earlier experts plus those of earlier parts.  Every workgroup reads
 // all counts, 8 experts of a part a load: thread t takes column t / side of
 // them and parts t % side, t % side + side, ....
-__global__ __launch_bounds__(kRouteThreads) void route_rows_kernel(RouteParams p, int parts, int chunks_per_part)
+__global__ __launch_bounds__(kRouteThreads) void route_rows_kernel(RouteParams p, int parts, int part_tokens)
 {
     __shared__ int s_before[kRouteMaxExperts], s_total[kRouteMaxExperts];
     __shared__ int s_wave[kRouteThreads / 64];
     const int tid = threadIdx.x, part = blockIdx.x;
     const int pitch = route_pitch(p.E), columns = pitch / 8;
-    const int64_t i0 = (int64_t)part * chunks_per_part * kRouteChunk * p.k;
-    const int64_t i1 = min(p.T * p.k, i0 + (int64_t)chunks_per_part * kRouteChunk * p.k);
+    const int64_t i0 = (int64_t)part * part_tokens * p.k;
+    const int64_t i1 = min(p.T * p.k, i0 + (int64_t)part_tokens * p.k);
     // this thread's first pair is on its way meanwhile
     const int64_t mine = min(i0 + tid, i1 - 1);
     const int first_id = p.topk_ids[mine], first_rank = p.row_of[mine];
@@ -361,15 +416,19 @@ __global__ __launch_bounds__(kThreads) void route_bwd_kernel(RouteBwdParams p)
     }
 }
 
-// Lanes per token, at least as many as slots.  For few tokens four experts a
-// lane: the shortest way through one token.  For many eight: a round of the
-// choice costs a wave about as much whether it holds one token or two (5000
-// tokens, 128 experts, softmax: 17.5 us with 32 lanes each, 8.0 with 16; 16384 of
-// 256, sigmoid: 20.8 with 64, 18.1 with 32).
+// Whether at most 64 tokens' experts are chosen by several workgroups before one orders them, which costs 0.9 us and
+// saves the time of a CU's share: 64 tokens, sigmoid, 8 of 60: 7.3 us alone, 8.0 with several; of 128: 10.0, 7.7; of 256:
+// 17.6, 7.6; of 1024: 52.6, 10.4; 16 tokens, 8 of 128: 6.5, 7.4; of 256: 8.3, 7.3.
+bool two_kernels(int64_t T, int E) { return T > 8 && T * E > 4096; }
+
+// Lanes per token, at least as many as slots.  Where tokens are few for the CUs at work, four experts a lane: the
+// shortest way through one token.  Otherwise eight: a round of the choice costs a wave about as much whether it holds
+// one token or two (5000 tokens, 128 experts, softmax: 17.5 us with 32 lanes each, 8.0 with 16; 16384 of 256, sigmoid:
+// 20.8 with 64, 18.1 with 32).
+bool few_lanes(const RouteParams &p) { return p.T <= 16 || (p.T <= kRouteChunk && two_kernels(p.T, p.E)); }
 template <class Run>
-hipError_t by_width(int64_t T, int E, int k, Run run)
+hipError_t by_width(bool few, int E, int k, Run run)
 {
-    const bool few = T <= 16;
     if (E <= 32 && k <= 8) run.template operator()<8, 4>();
     else if (E <= 64 && (few || k > 8)) run.template operator()<16, 4>();
     else if (E <= 64) run.template operator()<8, 8>();
@@ -382,17 +441,23 @@ hipError_t by_width(int64_t T, int E, int k, Run run)
 
 struct RunRoute {
     const RouteParams &p;
-    int parts, chunks;
+    int parts, part_tokens;
     RoutePlan plan;
     hipStream_t s;
     template <int LANES, int EPL>
     void operator()() const
     {
-        if (p.T <= kRouteChunk)
-            hipLaunchKernelGGL((route_one_kernel<LANES, EPL>), dim3(1), dim3(chunk_threads(EPL)), 0, s, p, plan);
-        else
+        constexpr int PER = kThreads / LANES;
+        if (p.T > kRouteChunk) {
             hipLaunchKernelGGL((route_kernel<LANES, EPL>), dim3((unsigned)parts), dim3(chunk_threads(EPL)), 0, s, p,
-                               chunks);
+                               part_tokens);
+        } else if (!two_kernels(p.T, p.E)) {
+            hipLaunchKernelGGL((route_one_kernel<LANES, EPL>), dim3(1), dim3(chunk_threads(EPL)), 0, s, p, plan);
+        } else {
+            hipLaunchKernelGGL((route_choose_kernel<LANES, EPL>), dim3((unsigned)((p.T + PER - 1) / PER)), dim3(kThreads),
+                               0, s, p);
+            hipLaunchKernelGGL(route_order_kernel, dim3(1), dim3(kOrderThreads), 0, s, p, plan);
+        }
     }
 };
 
@@ -408,26 +473,25 @@ struct RunRouteBwd {
     }
 };
 
-int64_t chunks_per_part(int64_t T)
+// Tokens of a part: few keep the choice short, but every part reads all parts' counts (8 of 256, sigmoid, with 64, 32
+// and 16 to a part: 1040 tokens 22.6 us, 16.0 and 13.6; 4100 tokens 26.6, 19.0 and 20.5).
+int part_tokens_of(int64_t T)
 {
-    const int64_t chunks = (T + kRouteChunk - 1) / kRouteChunk;
-    return (chunks + kRouteMaxParts - 1) / kRouteMaxParts;
+    const int64_t per = (T + kRouteMaxParts - 1) / kRouteMaxParts;
+    if (per > kRouteChunk) return (int)((per + kRouteChunk - 1) / kRouteChunk) * kRouteChunk;
+    return T <= 160 * 16 ? 16 : T <= 160 * 32 ? 32 : kRouteChunk;
 }
 
 }  // namespace
 
-int route_parts(int64_t T)
-{
-    const int64_t per = chunks_per_part(T) * kRouteChunk;
-    return T > 0 ? (int)((T + per - 1) / per) : 0;
-}
+int route_parts(int64_t T) { return (int)((T + part_tokens_of(T) - 1) / part_tokens_of(T)); }
 
 hipError_t launch_moe_route(const RouteParams &p, hipStream_t s)
 {
-    const int parts = route_parts(p.T), chunks = (int)chunks_per_part(p.T);
-    hipError_t e = by_width(p.T, p.E, p.k, RunRoute{p, parts, chunks, RoutePlan{nullptr, 1}, s});
+    const int parts = route_parts(p.T), part_tokens = part_tokens_of(p.T);
+    hipError_t e = by_width(few_lanes(p), p.E, p.k, RunRoute{p, parts, part_tokens, RoutePlan{nullptr, 1}, s});
     if (e == hipSuccess && p.T > kRouteChunk) {
-        hipLaunchKernelGGL(route_rows_kernel, dim3((unsigned)parts), dim3(kRouteThreads), 0, s, p, parts, chunks);
+        hipLaunchKernelGGL(route_rows_kernel, dim3((unsigned)parts), dim3(kRouteThreads), 0, s, p, parts, part_tokens);
         e = hipGetLastError();
     }
     return e;
@@ -435,12 +499,12 @@ hipError_t launch_moe_route(const RouteParams &p, hipStream_t s)
 
 hipError_t launch_moe_route_plan(const RouteParams &p, const RoutePlan &plan, hipStream_t s)
 {
-    return by_width(p.T, p.E, p.k, RunRoute{p, 1, 1, plan, s});
+    return by_width(few_lanes(p), p.E, p.k, RunRoute{p, 1, 0, plan, s});
 }
 
 hipError_t launch_moe_route_bwd(const RouteBwdParams &p, hipStream_t s)
 {
-    return by_width(0, p.E, p.k, RunRouteBwd{p, s});      // its loads and stores want whole lines of a token
+    return by_width(true, p.E, p.k, RunRouteBwd{p, s});   // its loads and stores want whole lines of a token
 }
 
 }  // namespace ptgg

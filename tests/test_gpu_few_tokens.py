@@ -123,6 +123,15 @@ def test_layer(dev, T, E, H, I, k, kind):
     check(x, z.bfloat16(), bias, ops, k, 1, int(k > 1), 2.5, kind)
 
 
+@pytest.mark.parametrize("T,E,k", [(40, 256, 6), (64, 100, 16), (9, 600, 4)])
+def test_many_experts(dev, T, E, k):
+    """The choice of experts by several workgroups, and tokens without any."""
+    x, z, bias, ops = make(dev, T, E, 96, 64, "mxfp8", T + E)
+    check(x, z, bias, ops, k, 1, 1, 2.5, "mxfp8")
+    z[T // 2:] = NINF
+    check(x, z, None, ops, k, 0, 0, 1.0, "mxfp8")
+
+
 @pytest.mark.parametrize("T,E,H,I,k", [(3, 4, 40, 24, 2), (20, 2, 72, 8, 2), (1, 3, 8, 16, 3), (18, 3, 264, 200, 2)])
 def test_bf16_widths_in_eights(dev, T, E, H, I, k):
     x, z, _, ops = make(dev, T, E, H, I, "bf16", T + H)

@@ -119,6 +119,26 @@ def test_route(dev, T, E, k, gate, renorm):
         check(z, b, k, gate, renorm, 2.5, got)
 
 
+# up to 64 tokens whose choice is spread over workgroups, and parts of 16, of an odd number and of 64 tokens
+@pytest.mark.parametrize("T,E,k", [(9, 1024, 16), (17, 256, 8), (33, 250, 5), (48, 100, 6), (64, 65, 12), (64, 257, 3), (300, 64, 4),
+                                   (2500, 40, 4), (4101, 72, 6), (9000, 20, 2)])
+@pytest.mark.parametrize("gate", [0, 1], ids=["softmax", "sigmoid"])
+def test_choice_spread_over_workgroups(dev, T, E, k, gate):
+    z, bias = logits(dev, T, E, T * 3 + E, "f32" if T % 2 else "bf16", shut=2)
+    b = bias if gate else None
+    got = route(z, b, k, gate, 1, 1.5)
+    assert got["err"] == 0
+    check(z, b, k, gate, 1, 1.5, got)
+    z[T - 1, 3] = float("nan")
+    z[T // 2] = NINF
+    got = route(z, b, k, gate, 0, 1.5)
+    assert got["err"] == 16
+    check(z, b, k, gate, 0, 1.5, got)
+    if T <= 64:
+        bare = route(z, b, k, gate, 0, 1.5, ws=None)
+        assert all(torch.equal(bare[n], got[n]) for n in bare)
+
+
 def test_many_tokens_per_part(dev):
     # more than 256 chunks of 64 tokens: parts of several chunks
     z, _ = logits(dev, 40000, 24, 3, "bf16")
