@@ -22,7 +22,6 @@ constexpr int kCuWaves = 16;              // that a CU holds of these kernels, i
 constexpr int kCuLds = 160 * 1024;
 constexpr int kRows = 16;                 // weight rows of a tile
 constexpr int kDepth = 4;                 // units of 2 KB that a wave keeps in flight
-constexpr int kStage = 2;                 // 16-byte pieces of the token rows a thread has in flight
 constexpr int kScalePieces = 3;           // 8-byte pieces of scales a thread moves
 
 // Elements in 16 bytes of a row, and in a unit, the reduction's step: a whole
@@ -43,13 +42,17 @@ __host__ __device__ constexpr int scale_region(int K, int wt, int waves, int spl
 // How a product is laid over the waves: `splits` waves share a tile's
 // reduction, a workgroup does waves / splits tiles (a group).  A wave's stream
 // should hold some 16 KB -- twice its ring; longer ones leave too few workgroups
-// to share out evenly, shorter ones are all start and end -- but the k experts
-// of a single token should keep 512 waves.  Measured, FC1 / FC2 in us with 1,
-// 2, 4, 8 waves to a tile: 1 token, 4 experts of 2880 x 2880 bf16 (92 KB tiles):
-// 24.8 / 22.8, 26.8 / 14.4, 22.4 / 15.2, 22.5 / 13.2; 7 tokens, 4096 x 2048
-// MXFP4 (32 and 16 KB): 49 / 27, 47 / 31, 58 / 48, 95 / 88; 64 tokens, the same in
-// bf16 (131 and 65 KB): 551 / 307, 570 / 281, 558 / 291, 604 / 320.  The number of
-// tokens does not enter: a token's sums do not depend on who shares its call.
+// to share out evenly, shorter ones are all start and end.  The k experts of a
+// single token should still keep 512 waves while that leaves a stream 8 KB, and
+// 256 in any case.  Measured, FC1 / FC2 in us with 1, 2, 4, 8 waves to a tile:
+// 1 token, 4 experts of 2880 x 2880 bf16 (92 KB tiles): 24.8 / 22.8, 26.8 / 14.4,
+// 22.4 / 15.2, 22.5 / 13.2; 7 tokens, 4096 x 2048 MXFP4 (32 and 16 KB): 49 / 27,
+// 47 / 31, 58 / 48, 95 / 88; 64 tokens, the same in bf16 (131 and 65 KB): 551 / 307,
+// 570 / 281, 558 / 291, 604 / 320.  The layer, where 256 or 512 waves are asked for
+// whatever the stream: 24 tokens on 2 of 60 MXFP4 experts of 2016 x 1504 (16 and 12
+// KB) 43.2 and 46.3, 16 on 3 of 8 MXFP8 of 1056 x 800 (17 and 13 KB) 20.6 and 19.7.
+// The number of tokens does not enter: a token's sums do not depend on who shares
+// its call.
 struct Layout {
     int tiles, splits, groups, lds_fixed;
 };
@@ -58,9 +61,10 @@ Layout layout_of(int tiles, int k, int K, int wt, int waves)
     int s = 1;
     const int bytes = kRows * row_bytes(K, wt);
     const auto scales = [&] { return scale_region(K, wt, kCuWaves, s); };   // of workgroups that fill a CU
+    const auto short_of_waves = [&] { return (int64_t)tiles * k * s < (bytes / (2 * s) >= 8 * 1024 ? 512 : 256); };
     while (units_of(K, wt) >= 2 * s &&
            (scales() > kCuWaves * 64 * 8 * kScalePieces ||
-            (s < 4 && (bytes / (2 * s) >= 15 * 1024 || (int64_t)tiles * k * s < 512))))
+            (s < 4 && (bytes / (2 * s) >= 15 * 1024 || short_of_waves()))))
         s *= 2;
     const int fixed = scale_region(K, wt, waves, s) + (s > 1 ? waves * 64 * 16 : 0);   // and the partial sums
     return {tiles, s, (tiles * s + waves - 1) / waves, fixed};
@@ -137,6 +141,9 @@ __device__ __forceinline__ void mma_unit(const uintx4 lo, const uintx4 hi, uint3
 // weights' stream is started.
 template <int THREADS>
 struct Stage {
+    // 16-byte pieces a thread has in flight: the large workgroups hold many rows (64 tokens, 8 experts of 4032 x 1984
+    // bf16: 196 us with 2, 188 with 4), the small ones few (12 tokens, 60 of 736 x 608 8 bits: 24.4 and 25.2)
+    static constexpr int kStage = THREADS == 64 * kCuWaves ? 4 : 2;
     uintx4 v[kStage];
     int at;
     template <class Row>
@@ -263,10 +270,13 @@ __device__ __forceinline__ void block_product(uint8_t *lds, const uint8_t *w, co
         const int u = start + done + i;
         return u >= n ? u - n : u;
     };
-    const auto load = [&](int i, int unit) {
+    const auto load = [&](int i, int unit, bool fill = false) {
         const int u = unit_at(unit);
         const uint32_t b = cut && u == n - 1 - (PATH == kTurned ? 0 : done) ? back : 0;
         const uintx4 *p = (const uintx4 *)(wp + u * 128 + (off - b)), *q = (const uintx4 *)(wp + u * 128 + (off_hi - b));
+        // what a short stream leaves of the ring: one piece for all lanes, which nothing uses (a branch would make the
+        // waits below count on fewer loads)
+        if (fill && unit >= n) p = q = (const uintx4 *)w;
         lo[i] = NT ? __builtin_nontemporal_load(p) : *p;
         __builtin_amdgcn_sched_barrier(0);
         hi[i] = NT ? __builtin_nontemporal_load(q) : *q;
@@ -274,7 +284,7 @@ __device__ __forceinline__ void block_product(uint8_t *lds, const uint8_t *w, co
     };
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int i = 0; i < kDepth; ++i) load(i, min(i, n - 1));
+    for (int i = 0; i < kDepth; ++i) load(i, i, true);
 
     st.finish(s_x, pitch, m);
     if constexpr (MX) {
@@ -471,15 +481,15 @@ hipError_t launch_products(const FewParams &p, const Layout &l1, const Layout &l
 hipError_t launch_few_tokens(const FewParams &p, hipStream_t s)
 {
     // The waves of a workgroup share its tokens' rows and its LDS.  Small workgroups hide each other's starts and end
-    // evenly, which counts where little is read; large ones copy the tokens less often and hold more of them, and an expert
-    // of more rows than they hold is read once for every block of them.  In us with 4, 8 and 16 waves: 1 token, 4 of 32
-    // experts, 2880 x 2880 bf16: 45.4, 47.9, 54.6; 10 tokens, 6 of 60, 1440 x 992 4 bits: 30.2, 32.0, -; 24 tokens, 6 of
-    // 256, 4032 x 1984 4 bits: 216, 210, -; 33 tokens, 4 of 32, 2880 x 2880 8 bits: 155, 133, 145; 64 tokens, 6 of 8, 4032 x
-    // 1984 bf16 (8 waves: one workgroup a CU): -, 236, 194.  The sums are the same.
+    // evenly, which counts where little is read; large ones copy the tokens less often and hold more of them, and an
+    // expert of more rows than they hold is read once for every block of them.  In us with 4, 8 and 16 waves: 1 token, 4
+    // of 32 experts, 2880 x 2880 bf16: 45.4, 47.9, 54.6; 64 tokens, 6 of 256, 1056 x 544 4 bits: 62.7, 67.9, -; 24 tokens, 6
+    // of 256, 4032 x 1984 4 bits: 216, 210, -; 33 tokens, 4 of 32, 2880 x 2880 8 bits: 155, 133, 145; 64 tokens, 6 of 8,
+    // 4032 x 1984 bf16 (8 waves: one workgroup a CU): -, 236, 194.  The sums are the same.
     Layout l1, l2;
     const int pairs = p.T * p.k;
     const int64_t expert = 2 * (int64_t)p.I * row_bytes(p.H, p.weights) + (int64_t)p.H * row_bytes(p.I, p.weights);
-    int cap = 0, waves = pairs <= p.E && pairs * expert <= (int64_t)1 << 29 ? 4 : 8;
+    int cap = 0, waves = pairs <= 2 * p.E && pairs * expert <= (int64_t)1 << 29 ? 4 : 8;
     for (;; waves *= 2) {
         l1 = layout_of(p.I / 8, p.k, p.H, p.weights, waves);
         l2 = layout_of((p.H + kRows - 1) / kRows, p.k, p.I, p.weights, waves);
