@@ -608,8 +608,8 @@ size_t pt_grouped_gemm_workspace_size(int op, int64_t G, int64_t M, int64_t N,
  *               codes, both NULL
  *  rstd         [rows] fp32 for the backward, or NULL
  *  stream_dtype PT_BF16 or PT_FP32
- * A row of zeros has rstd = eps^-1/2 and zero outputs (block exponent 0, row
- * factor 1).  A row that holds a NaN or an infinity gives NaNs in y and in
+ * A row of zeros has rstd = eps^-1/2 and, where eps > 0, zero outputs (block
+ * exponent 0, row factor 1).  A row that holds a NaN or an infinity gives NaNs in y and in
  * its codes.
  *  Requirements: cols % 8 == 0 (cols % 32 == 0 for MXFP8), cols <= 32768,
  *  rows <= 2^23, eps >= 0; x, residual, weight, residual_out, y and q 16-byte
@@ -650,7 +650,7 @@ size_t pt_rmsnorm_workspace_size(int64_t rows, int64_t cols);
  *  PT_GATE_SIGMOID  score = sigmoid(logit) + bias, rounded to fp32 once;
  *                   weight = sigmoid(logit) (no bias), with renorm divided by
  *                   the sum over the chosen ones
- * and every weight times `scale`.  An expert whose logit is -inf or NaN is not
+ * and every weight times `scale`.  An expert whose logit (or bias) is -inf or NaN is not
  * chosen (a NaN also sets error bit 4); a token with fewer than k experts left
  * gets id -1 and weight 0 in the slots past them.
  * A logit of +inf is chosen first; among softmax scores it makes the token's

@@ -235,6 +235,32 @@ def test_gradient_against_differences(dev):
     assert abs(numeric - ours) <= slack
 
 
+def test_elements_past_32_bits(dev):
+    """More than 2^31 elements: the last rows like a call of their own, and a weight gradient that only they feed."""
+    rows, cols, k = 65600, 32768, 40
+    x, s, w = inputs(dev, k, cols, "bf16", 41)
+    big = {n: torch.zeros((rows, cols), dtype=torch.bfloat16, device=dev) for n in ("x", "s", "h", "y")}
+    big["x"][-k:], big["s"][-k:] = x, s
+    q = torch.empty((rows, cols), dtype=torch.uint8, device=dev)
+    scales, rstd = torch.empty((rows, cols // 32), dtype=torch.uint8, device=dev), torch.empty(rows, device=dev)
+    ptm.pt_rmsnorm_fwd(big["x"], big["s"], w, big["h"], big["y"], q, scales, rstd, rows, cols, 1e-5, ptm.PT_BF16,
+                       ptm.PT_MXFP8_E4M3)
+    ref = forward(x, s, w, "bf16", "mxfp8")
+    for got, want in ((big["h"], "h"), (big["y"], "y"), (q, "q"), (scales, "scales"), (rstd, "rstd")):
+        assert torch.equal(got[-k:], ref[want])
+    assert big["y"][:-k].eq(0).all() and q[:-k].eq(0).all()
+    dy = big["x"]                                        # zero but for the last rows
+    n = ptm.pt_rmsnorm_workspace_size(rows, cols)
+    ds, dw = big["y"], torch.empty(cols, device=dev)
+    ptm.pt_rmsnorm_bwd(dy, big["h"], w, rstd, None, ds, dw, rows, cols, ptm.PT_BF16, 0,
+                       workspace=torch.empty(n, dtype=torch.uint8, device=dev))
+    rds, rdw = backward(x, ref["h"], w, ref["rstd"], None, "bf16")
+    assert torch.equal(ds[-k:], rds) and ds[:-k].eq(0).all()
+    # the same terms in another order: at most k additions, each off by 2^-24 of the sum of their sizes
+    _, _, _, size = backward_reference(x, ref["h"], w, ref["rstd"], None)
+    assert ((dw.to(F64) - rdw.to(F64)).abs() <= 2 * (k + 4) * 2.0 ** -24 * size).all()
+
+
 def test_streams_and_graph(dev):
     """On a side stream, and captured: every replay gives the eager bits."""
     x, s, w = inputs(dev, 100, 2880, "bf16", 31)

@@ -200,6 +200,45 @@ def test_nan_is_never_chosen_and_is_reported(dev, gate):
 
 
 @pytest.mark.parametrize("T", [10, 100])
+def test_infinite_biases(dev, T):
+    z, bias = logits(dev, T, 64, 15)
+    bias[5] = NINF
+    check(z, bias, 4, 1, 1, 1.0, route(z, bias, 4, 1, 1, 1.0))
+    bias[[9, 40]] = float("inf")                         # fewer than are chosen, then more
+    check(z, bias, 4, 1, 0, 1.0, route(z, bias, 4, 1, 0, 1.0))
+    bias[50:60] = float("inf")
+    check(z, bias, 4, 1, 1, 1.0, route(z, bias, 4, 1, 1, 1.0))
+
+
+def test_logits_past_32_bits(dev):
+    """More than 2^31 logits: the last tokens' choices and gradients, and the counts."""
+    T, E, k = 2_100_000, 1024, 2
+    z = torch.zeros((T, E), dtype=torch.bfloat16, device=dev)
+    tail, _ = logits(dev, 500, E, 16, "bf16")
+    z[-500:] = tail
+    n = ptm.pt_moe_route_workspace_size(T, E, k)
+    ids, w = torch.empty((T, k), dtype=torch.int32, device=dev), torch.empty((T, k), device=dev)
+    lens, row_of = torch.empty(E, dtype=torch.int64, device=dev), torch.empty((T, k), dtype=torch.int32, device=dev)
+    token_of = torch.empty(T * k, dtype=torch.int32, device=dev)
+    ptm.pt_moe_route(z, None, ids, w, lens, row_of, token_of, T, E, k, ptm.PT_BF16, 0, 1, 1.0,
+                     workspace=torch.zeros(n, dtype=torch.uint8, device=dev))
+    rids, rw = choose64(tail, None, k, 0, 1, 1.0)
+    assert torch.equal(ids[-500:].cpu(), rids) and ((w[-500:].cpu().to(F64) - rw).abs() <= TOL * rw).all()
+    assert ids[:-500].eq(torch.tensor([0, 1], device=dev, dtype=torch.int32)).all()
+    flat = ids.flatten().long()
+    assert torch.equal(lens, torch.bincount(flat, minlength=E))
+    order = torch.argsort(flat, stable=True)
+    assert torch.equal(token_of.long(), order // k)
+    assert torch.equal(row_of.flatten()[order].long(), torch.arange(T * k, device=dev))
+    dw = torch.ones((T, k), device=dev)
+    dw[:, 1] = -1.0
+    dz = torch.empty_like(z)
+    ptm.pt_moe_route_bwd(z, ids, dw, dz, T, E, k, ptm.PT_BF16, 0, 1, 1.0)
+    alone = backward(tail, ids[-500:].contiguous(), dw[-500:].contiguous(), 0, 1, 1.0)
+    assert torch.equal(dz[-500:], alone)
+
+
+@pytest.mark.parametrize("T", [10, 100])
 def test_plus_infinity_is_chosen_first(dev, T):
     z, _ = logits(dev, T, 64, 14)
     z[1, 7] = float("inf")
