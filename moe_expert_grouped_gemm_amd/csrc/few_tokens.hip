@@ -483,20 +483,23 @@ hipError_t launch_few_tokens(const FewParams &p, hipStream_t s)
     // The waves of a workgroup share its tokens' rows and its LDS.  Small workgroups hide each other's starts and end
     // evenly, which counts where little is read; large ones copy the tokens less often and hold more of them, and an
     // expert of more rows than they hold is read once for every block of them.  In us with 4, 8 and 16 waves: 1 token, 4
-    // of 32 experts, 2880 x 2880 bf16: 45.4, 47.9, 54.6; 64 tokens, 6 of 256, 1056 x 544 4 bits: 62.7, 67.9, -; 24 tokens, 6
-    // of 256, 4032 x 1984 4 bits: 216, 210, -; 33 tokens, 4 of 32, 2880 x 2880 8 bits: 155, 133, 145; 64 tokens, 6 of 8,
-    // 4032 x 1984 bf16 (8 waves: one workgroup a CU): -, 236, 194.  The sums are the same.
+    // of 32 experts, 2880 x 2880 bf16: 45.4, 47.9, 54.6; 64 tokens, 6 of 256, 1056 x 544 4 bits: 62.7, 67.9, -; 40, 6 of
+    // 256, 2016 x 992 4 bits: 93.7, 96.9, -; 24, 6 of 256, 4032 x 1984 4 bits: 224, 217, -; 5, 3 of 8, 4000 x 1952 bf16:
+    // 62.7, 58.6, -; 33, 4 of 32, 2880 x 2880 8 bits: 155, 133, 145; 64, 6 of 8, 4032 x 1984 bf16 (8 waves: one workgroup
+    // a CU): -, 236, 194.  The sums are the same.
     Layout l1, l2;
     const int pairs = p.T * p.k;
     const int64_t expert = 2 * (int64_t)p.I * row_bytes(p.H, p.weights) + (int64_t)p.H * row_bytes(p.I, p.weights);
-    int cap = 0, waves = pairs <= 2 * p.E && pairs * expert <= (int64_t)1 << 29 ? 4 : 8;
+    int cap = 0, waves = pairs <= 2 * p.E && pairs * expert <= (int64_t)1 << 30 ? 4 : 8;
     for (;; waves *= 2) {
         l1 = layout_of(p.I / 8, p.k, p.H, p.weights, waves);
         l2 = layout_of((p.H + kRows - 1) / kRows, p.k, p.I, p.weights, waves);
         const int per_cu = kCuWaves / waves;
         const int c1 = row_cap(l1, p.H, p.weights, p.T, per_cu), c2 = row_cap(l2, p.I, p.weights, p.T, per_cu);
         cap = c1 < c2 ? c1 : c2;
-        if (waves == kCuWaves || (cap >= 1 && pairs <= p.E * cap && l1.splits <= waves && l2.splits <= waves)) break;
+        // rows an expert may have on average; of 4 waves' LDS a third, since few tokens spread unevenly
+        const int room = waves == 4 && cap < p.T ? p.E * cap / 3 : p.E * cap;
+        if (waves == kCuWaves || (cap >= 1 && pairs <= room && l1.splits <= waves && l2.splits <= waves)) break;
     }
     hipError_t e = launch_moe_route_plan(p.route, RoutePlan{p.plan, cap}, s);
     if (e != hipSuccess) return e;
