@@ -653,6 +653,8 @@ size_t pt_rmsnorm_workspace_size(int64_t rows, int64_t cols);
  * and every weight times `scale`.  An expert whose logit (or bias) is -inf or NaN is not
  * chosen (a NaN also sets error bit 4); a token with fewer than k experts left
  * gets id -1 and weight 0 in the slots past them.
+ * A mask of fp32's lowest value, in a logit or a bias, is a number: such an
+ * expert is chosen where too few others are left.
  * A logit of +inf is chosen first; among softmax scores it makes the token's
  * weights NaN.
  *  logits       [T, E] fp32 or bf16 (logits_dtype PT_FP32 or PT_BF16)

@@ -147,6 +147,15 @@ __device__ __forceinline__ float logit_at(const void *logits, int bf16, int64_t 
     return bf16 ? bf16_to_f32(((const uint16_t *)logits)[i]) : ((const float *)logits)[i];
 }
 
+// The least 32-bit score that may belong among the chosen once scores are exact, given the k-th one's.  A sigmoid is off
+// by less than 2^-22 (|z| v (1 - v) < 1/4 bounds the exponent's rounding, and three more roundings of 2^-24), the sum
+// with the bias by a rounding: less than half of the margin.  Never -inf, which is what a score has that must not be
+// chosen, also where the k-th is next to fp32's lowest value (experts masked by their bias).
+__host__ __device__ __forceinline__ float candidate_floor(float kth)
+{
+    return __builtin_fmaxf(kth - 0x1p-20f * (1.0f + __builtin_fabsf(kth)), -3.40282346638528859812e+38f);
+}
+
 // What a slot's lane knows of its expert.
 struct Slot {
     int id;                   // -1: none
@@ -197,9 +206,9 @@ __device__ __forceinline__ Slot take_largest(int k, uint32_t (&key)[EPL])
 // weight.  nan: a NaN among the scores.
 //
 // Sigmoid scores are ordered as 64 bits rounded to 32 give them, which is dear
-// for every expert.  Scores in 32 bits, off by less than half of `margin`, name
-// the candidates; where exactly k of them reach the k-th one's neighbourhood,
-// only those are computed in 64 bits and put in order, else all that do.
+// for every expert.  Scores in 32 bits name the candidates; where exactly k of
+// them reach the k-th one's neighbourhood (candidate_floor), only those are
+// computed in 64 bits and put in order, else all that do.
 template <int LANES, int EPL>
 __device__ __forceinline__ void choose(const RouteParams &p, int64_t t, const float (&z)[EPL], const float (&bias)[EPL],
                                        int &id, float &weight, bool &nan)
@@ -240,19 +249,17 @@ __device__ __forceinline__ void choose(const RouteParams &p, int64_t t, const fl
         key[i] = score_key(near[i]);
     }
     Slot s = take_largest<LANES, EPL>(p.k, key);
-    // a sigmoid is off by less than 2^-22 (|z| v (1 - v) < 1/4 bounds the exponent's rounding, and three more
-    // roundings of 2^-24), the sum with the bias by a rounding
     const uint32_t kth = group_max_u32<LANES>(sub == p.k - 1 ? s.key : 0u);
-    const float low = key_score(kth), margin = 0x1p-20f * (1.0f + __builtin_fabsf(low));
+    const float floor = candidate_floor(key_score(kth));
     bool close = false;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) close |= kth != 0 && key[i] != 0 && near[i] >= low - margin;
+    for (int i = 0; i < EPL; ++i) close |= kth != 0 && key[i] != 0 && near[i] >= floor;
     double v;
     if (group_max_u32<LANES>(close ? 1u : 0u)) {               // one that was not taken is near
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
             key[i] = 0;                                        // the others lie lower for certain
-            if (near[i] >= low - margin) key[i] = score_key((float)(sigmoid64(z[i]) + (double)bias[i]));
+            if (near[i] >= floor) key[i] = score_key((float)(sigmoid64(z[i]) + (double)bias[i]));
         }
         s = take_largest<LANES, EPL>(p.k, key);
         id = s.id;
