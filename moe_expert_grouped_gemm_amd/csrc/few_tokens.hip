@@ -23,6 +23,7 @@ constexpr int kCuLds = 160 * 1024;
 constexpr int kRows = 16;                 // weight rows of a tile
 constexpr int kDepth = 4;                 // units of 2 KB that a wave keeps in flight
 constexpr int kScalePieces = 3;           // 8-byte pieces of scales a thread moves
+constexpr int kTurns = 4;                 // places of a row where tiles start that would meet in memory's channels
 
 // Elements in 16 bytes of a row, and in a unit, the reduction's step: a whole
 // 128-byte line of each of the tile's rows.
@@ -51,8 +52,8 @@ __host__ __device__ constexpr int scale_region(int K, int wt, int waves, int spl
 // 570 / 281, 558 / 291, 604 / 320.  The layer, where 256 or 512 waves are asked for
 // whatever the stream: 24 tokens on 2 of 60 MXFP4 experts of 2016 x 1504 (16 and 12
 // KB) 43.2 and 46.3, 16 on 3 of 8 MXFP8 of 1056 x 800 (17 and 13 KB) 20.6 and 19.7.
-// The number of tokens does not enter: a token's sums do not depend on who shares
-// its call.
+// The number of tokens does not enter, here or in where a stream starts (Path): a
+// token's sums do not depend on who shares its call.
 struct Layout {
     int tiles, splits, groups, lds_fixed;
 };
@@ -208,9 +209,12 @@ struct Rows {
 // caches (2880-byte rows: 87.7 us cached, 94.1 not; 2048-byte rows: 51.6 and
 // 48.5).  kLines: whole lines, each of them read once.  kTurned: also a multiple
 // of 4096 bytes apart, so that waves at the same unit of their rows would meet
-// in a few of the memory's channels: each tile of a workgroup starts at another
-// unit and goes round (8192-byte rows: 614 -> 548 us; the turn costs the
-// others 1%).
+// in a few of the memory's channels: consecutive tiles start at kTurns places of
+// their rows and go round (8192-byte rows: 614 -> 548 us; the turn costs the
+// others 1%).  The place follows from the tile's number alone, not from the tiles
+// of a workgroup, whose waves follow from the number of tokens: a token's sums
+// keep their order.  With 2, 4, 8 and 16 places: 178.4, 177.8, 178.4, 179.1 us
+// (geometric mean of 12 layers of 1 to 64 tokens).
 enum Path { kShared = 0, kLines = 1, kTurned = 2 };
 
 // The products of one block with a group of tiles, one to `splits` waves.  A
@@ -232,7 +236,8 @@ __device__ __forceinline__ void block_product(uint8_t *lds, const uint8_t *w, co
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int splits = l.splits, tiles = WAVES / splits, split = wave % splits, slot = wave / splits;
     const int first = units * split / splits;
-    const int n = units * (split + 1) / splits - first, start = PATH == kTurned ? n * slot / tiles : 0;
+    const int tile = group * tiles + slot, n = units * (split + 1) / splits - first;
+    const int start = PATH == kTurned ? n * (tile % kTurns) / kTurns : 0;
     uint8_t *s_part = lds, *s_scale = lds + (splits > 1 ? THREADS * 16 : 0);
     const int region = MX ? tiles * kRows * sb : 0;
     uint8_t *s_x = s_scale + region;
@@ -254,7 +259,7 @@ __device__ __forceinline__ void block_product(uint8_t *lds, const uint8_t *w, co
 
     // the stream: a scalar address and the lanes' offsets from it; past the last tile: that one again.  The last
     // tile of FC2 may have 8 rows only: those twice.
-    const int tile = group * tiles + slot, t = min(tile, l.tiles - 1);
+    const int t = min(tile, l.tiles - 1);
     const uint8_t *wp = w + (int64_t)t * geo.step * rb + first * 128;
     const uint32_t off = (uint32_t)geo.row(lane & 7) * rb + piece * 16;
     const uint32_t off_hi = off + (uint32_t)((PHASE == 2 && t * kRows + 8 >= geo.rows) ? 0 : geo.half * rb);
