@@ -90,6 +90,20 @@ __device__ __forceinline__ float group_sum(float x)
 {
     return bits_f32(group_reduce<LANES>(f32_bits(x), [](uint32_t a, uint32_t b) { return f32_bits(bits_f32(a) + bits_f32(b)); }));
 }
+// Sum of a lane's f(0) .. f(EPL - 1): fours one after another, then pairs of them, as four to a lane are joined across
+// lanes, so that the bits are the same however many a lane holds.
+template <int EPL, class F>
+__device__ __forceinline__ float fours_sum(F f)
+{
+    float s[EPL / 4];
+#pragma unroll
+    for (int i = 0; i < EPL / 4; ++i) s[i] = ((f(4 * i) + f(4 * i + 1)) + f(4 * i + 2)) + f(4 * i + 3);
+#pragma unroll
+    for (int n = 1; n < EPL / 4; n *= 2)
+#pragma unroll
+        for (int i = 0; i + n < EPL / 4; i += 2 * n) s[i] += s[i + n];
+    return s[0];
+}
 // x of the group's lane j, in every lane.
 template <int LANES>
 __device__ __forceinline__ uint32_t group_lane(uint32_t x, int j)
@@ -233,10 +247,7 @@ __device__ __forceinline__ void choose(const RouteParams &p, int64_t t, const fl
         if (p.renorm) {
             total = slots_sum<LANES>(e);
         } else {
-            total = 0.0f;
-#pragma unroll
-            for (int i = 0; i < EPL; ++i) total += z[i] > ninf ? expf(z[i] - m) : 0.0f;
-            total = group_sum<LANES>(total);
+            total = group_sum<LANES>(fours_sum<EPL>([&](int i) { return z[i] > ninf ? expf(z[i] - m) : 0.0f; }));
         }
         weight = id >= 0 ? e / total * p.scale : 0.0f;
         return;

@@ -5,7 +5,8 @@ and lanes the two calls are given.
 import pytest
 import torch
 
-from test_gpu_few_tokens import run
+from test_gpu_few_tokens import KINDS, make, run
+from test_gpu_route import logits, route
 
 pytestmark = pytest.mark.gpu
 
@@ -37,3 +38,25 @@ def test_rows_whose_tiles_take_turns(dev, T, kind, H, I):
     alone = torch.cat([run(x[t:t + 1].clone(), z[t:t + 1].clone(), None, w1, s1, w2, s2, 2, 0, 1, 1.0, kind)[0]
                        for t in range(T)])
     assert many.float().isfinite().all() and torch.equal(alone, many)
+
+
+@pytest.mark.parametrize("E,k", [(20, 8), (30, 10), (60, 4), (64, 9), (100, 5), (128, 6), (256, 6), (250, 16), (512, 6), (1024, 4)])
+@pytest.mark.parametrize("gate", [0, 1], ids=["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [0, 1])
+def test_router(dev, E, k, gate, renorm):
+    """The choice and the weights, with as many lanes and experts to a lane as each number of tokens gets."""
+    z, bias = logits(dev, 300, E, E + k)
+    b = bias if gate else None
+    many = route(z, b, k, gate, renorm, 2.5)
+    for T in (1, 12, 20, 40, 64, 130):
+        few = route(z[:T].clone(), b, k, gate, renorm, 2.5)
+        assert torch.equal(few["ids"], many["ids"][:T]) and torch.equal(few["w"], many["w"][:T]), T
+
+
+@pytest.mark.parametrize("kind", sorted(KINDS))
+def test_layer_with_shares_of_all_experts(dev, kind):
+    x, z, _, (a, b) = make(dev, 40, 128, 96, 64, kind, 43)
+    many, _, w = run(x, z, None, a[0], a[1], b[0], b[1], 6, 0, 0, 1.0, kind)
+    for T in (1, 20):
+        few, _, v = run(x[:T].clone(), z[:T].clone(), None, a[0], a[1], b[0], b[1], 6, 0, 0, 1.0, kind)
+        assert torch.equal(v, w[:T]) and torch.equal(few, many[:T])
