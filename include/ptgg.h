@@ -697,8 +697,9 @@ int pt_moe_route_bwd(const void *logits, const int32_t *topk_ids, const float *d
  *                    (bf16(silu(gate) * up) . w2[e]^T) ),  e = topk_ids[t, j],
  *     [gate | up] = x[t] . w1[e]^T
  * with fp32 sums and the SwiGLU (and swiglu_limit) of pt_grouped_gemm_fwd's
- * PT_EPI_SWIGLU.  Only the chosen experts' weights are read.  A token without
- * experts gives zeros.
+ * PT_EPI_SWIGLU, where a gate or an up value that is NaN makes the token's
+ * output NaN, whatever swiglu_limit.  Only the chosen experts' weights are
+ * read.  A token without experts gives zeros.
  *  x     [T, H] bf16;  logits [T, E];  out [T, H] bf16
  *  w1    [E, 2I, H], w2 [E, H, I]: bf16 (weight_dtype PT_BF16, scales NULL),
  *        or codes with E8M0 scales [E, 2I, H/32] and [E, H, I/32]

@@ -382,6 +382,13 @@ __device__ __forceinline__ const FewBlock *my_block(const int *plan, int &group)
     return b;
 }
 
+// silu_mul, but for NaNs: minima and maxima would make the clamp's limit of them.
+__device__ __forceinline__ float gated(float gate, float up, float lim)
+{
+    const float v = silu_mul(gate, up, lim);
+    return __builtin_isunordered(gate, up) ? __builtin_nanf("") : v;
+}
+
 template <int WT, int PATH, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, waves_per_simd(WT, WAVES)) void few_fc1_kernel(FewParams p, Layout l)
 {
@@ -398,7 +405,7 @@ __global__ __launch_bounds__(64 * WAVES, waves_per_simd(WT, WAVES)) void few_fc1
         [&](int i) { return p.x + (int64_t)((tokens[i >> 2] >> (8 * (i & 3))) & 0xFFu) * p.H; },
         [&](int tile, floatx4 c) {
             *(bf16x2_t *)(p.h + (int64_t)(row0 + r) * p.I + tile * 8 + 2 * g) =
-                bf16x2_t{(__bf16)silu_mul(c[0], c[2], p.swiglu_limit), (__bf16)silu_mul(c[1], c[3], p.swiglu_limit)};
+                bf16x2_t{(__bf16)gated(c[0], c[2], p.swiglu_limit), (__bf16)gated(c[1], c[3], p.swiglu_limit)};
         });
 }
 
