@@ -39,6 +39,12 @@ class MoeBlock:
     def _new(self, shape, dtype=torch.bfloat16):
         return torch.empty(shape, dtype=dtype, device=self.device)
 
+    def _rows(self, n):
+        """n rows for a product to fill and a zero one."""
+        rows = self._new((n + 1, self.H))
+        rows[n].zero_()
+        return rows
+
     def _gemm_workspace(self, op, rows, N, K):
         n = pt.pt_grouped_gemm_workspace_size(op, self.E, rows, N, K, pt.PT_BF16)
         return self._new(n, torch.uint8)
@@ -60,34 +66,40 @@ class MoeBlock:
         pt.pt_moe_route(logits, None, ids, weights, lens, row_of, token_of, T, E, k, pt.PT_FP32, pt.PT_GATE_SOFTMAX, 1,
                         workspace=self._new(pt.pt_moe_route_workspace_size(T, E, k), torch.uint8))
         M = T * k
+        # a token without experts (one that holds a NaN) has -1 in row_of and leaves the last rows to nobody: it reads row M,
+        # which is zero, and offs keeps the products to the rows that experts have
+        offs = torch.zeros(E + 1, dtype=torch.int64, device=self.device)
+        torch.cumsum(lens, 0, out=offs[1:])
+        row_of = torch.where(row_of < 0, M, row_of).long()
+        token_of.clamp_(min=0)
         a = y.index_select(0, token_of)
-        c, h, o = self._new((M, 2 * I)), self._new((M, I)), self._new((M, H))
-        pt.pt_grouped_gemm_fwd_swiglu_save(a, None, self.w1, None, h, c, lens, None, E, M, 2 * I, H, pt.PT_BF16, 1,
+        c, h, o = self._new((M, 2 * I)), self._new((M, I)), self._rows(M)
+        pt.pt_grouped_gemm_fwd_swiglu_save(a, None, self.w1, None, h, c, lens, offs, E, M, 2 * I, H, pt.PT_BF16, 1,
                                            workspace=self._gemm_workspace(pt.PT_OP_FWD, M, 2 * I, H))
-        pt.pt_grouped_gemm_fwd(h, None, self.w2, None, o, None, lens, None, E, M, H, I, pt.PT_BF16, 1, pt.PT_EPI_NONE,
+        pt.pt_grouped_gemm_fwd(h, None, self.w2, None, o, None, lens, offs, E, M, H, I, pt.PT_BF16, 1, pt.PT_EPI_NONE,
                                workspace=self._gemm_workspace(pt.PT_OP_FWD, M, H, I))
-        out = (o[row_of.long()].float() * weights.unsqueeze(2)).sum(1).bfloat16()
-        self.saved = (stream, y, rstd, logits, ids, weights, lens, row_of.long(), token_of, a, c, h, o)
+        out = (o[row_of].float() * weights.unsqueeze(2)).sum(1).bfloat16()
+        self.saved = (stream, y, rstd, logits, ids, weights, lens, row_of, token_of, a, c, h, o, offs)
         return out, stream
 
     def backward(self, dout, dstream):
         """The gradient of the block's inputs (x and the residual alike); the weights' gradients are added to self.grad.
         dstream: the gradient that reaches the residual stream past this block."""
-        stream, y, rstd, logits, ids, weights, lens, row_of, token_of, a, c, h, o = self.saved
+        stream, y, rstd, logits, ids, weights, lens, row_of, token_of, a, c, h, o, offs = self.saved
         T, k, E, H, I = y.shape[0], self.k, self.E, self.H, self.I
         M = T * k
         dweights = torch.stack([(o[row_of[:, j]].float() * dout.float()).sum(1) for j in range(k)], 1)
-        row_weight = self._new(M, torch.float32)
+        row_weight = torch.zeros(M + 1, device=self.device)
         row_weight[row_of.flatten()] = weights.flatten()
-        do = (dout.index_select(0, token_of).float() * row_weight.unsqueeze(1)).bfloat16()
-        dc, da = self._new((M, 2 * I)), self._new((M, H))
-        pt.pt_grouped_gemm_dgrad_swiglu(do, self.w2, c, dc, lens, None, E, M, H, I, 1,
+        do = (dout.index_select(0, token_of).float() * row_weight[:M].unsqueeze(1)).bfloat16()
+        dc, da = self._new((M, 2 * I)), self._rows(M)
+        pt.pt_grouped_gemm_dgrad_swiglu(do, self.w2, c, dc, lens, offs, E, M, H, I, 1,
                                         workspace=self._gemm_workspace(pt.PT_OP_DGRAD, M, H, I))
-        pt.pt_grouped_gemm_wgrad(h, None, do, None, self.grad["w2"], lens, None, E, M, H, I, pt.PT_BF16, 1, 1,
+        pt.pt_grouped_gemm_wgrad(h, None, do, None, self.grad["w2"], lens, offs, E, M, H, I, pt.PT_BF16, 1, 1,
                                  workspace=self._gemm_workspace(pt.PT_OP_WGRAD, M, H, I))
-        pt.pt_grouped_gemm_dgrad(dc, None, self.w1, None, da, lens, None, E, M, 2 * I, H, pt.PT_BF16, 1,
+        pt.pt_grouped_gemm_dgrad(dc, None, self.w1, None, da, lens, offs, E, M, 2 * I, H, pt.PT_BF16, 1,
                                  workspace=self._gemm_workspace(pt.PT_OP_DGRAD, M, 2 * I, H))
-        pt.pt_grouped_gemm_wgrad(a, None, dc, None, self.grad["w1"], lens, None, E, M, 2 * I, H, pt.PT_BF16, 1, 1,
+        pt.pt_grouped_gemm_wgrad(a, None, dc, None, self.grad["w1"], lens, offs, E, M, 2 * I, H, pt.PT_BF16, 1, 1,
                                  workspace=self._gemm_workspace(pt.PT_OP_WGRAD, M, 2 * I, H))
         dlogits = torch.empty_like(logits)
         pt.pt_moe_route_bwd(logits, ids, dweights, dlogits, T, E, k, pt.PT_FP32, pt.PT_GATE_SOFTMAX, 1)
