@@ -610,7 +610,9 @@ size_t pt_grouped_gemm_workspace_size(int op, int64_t G, int64_t M, int64_t N,
  *  stream_dtype PT_BF16 or PT_FP32
  * A row of zeros has rstd = eps^-1/2 and, where eps > 0, zero outputs (block
  * exponent 0, row factor 1).  A row that holds a NaN or an infinity gives NaNs in y and in
- * its codes.
+ * its codes.  The sum of squares is an fp32 value: where it passes 3.4e38 (entries of
+ * about 1e19) rstd and the outputs are zero, where it underflows and eps is 0 rstd is
+ * infinite.
  *  Requirements: cols % 8 == 0 (cols % 32 == 0 for MXFP8), cols <= 32768,
  *  rows <= 2^23, eps >= 0; x, residual, weight, residual_out, y and q 16-byte
  *  aligned.
@@ -704,11 +706,14 @@ int pt_moe_route_bwd(const void *logits, const int32_t *topk_ids, const float *d
  *  w1    [E, 2I, H], w2 [E, H, I]: bf16 (weight_dtype PT_BF16, scales NULL),
  *        or codes with E8M0 scales [E, 2I, H/32] and [E, H, I/32]
  *        (PT_MXFP8_E4M3, PT_MXFP4_E2M1: the layouts of pt_grouped_gemm_fwd
- *        with trans_b = 1)
+ *        with trans_b = 1); a weight's value is taken as bf16, which holds
+ *        it exactly from 2^-126 to 3.39e38 in size (below, in steps of
+ *        2^-133; above, infinite)
  *  topk_ids, topk_weights [T, k]: the router's, as outputs
  *  workspace  required: pt_moe_few_tokens_workspace_size(T, E, H, I, k) bytes,
  *        16-byte aligned (word 0 takes the error bits)
- *  Deterministic.  Requirements: H and I % 8 == 0 (bf16) or % 32 == 0 (MX),
+ *  Deterministic, and a token's bits are those of a call of its own.
+ *  Requirements: H and I % 8 == 0 (bf16) or % 32 == 0 (MX),
  *  H and I <= 16384; x, logits, bias, w1, w2 and out 16-byte aligned; the others as
  *  pt_moe_route.  A weight tensor may exceed 2 GiB.
  */

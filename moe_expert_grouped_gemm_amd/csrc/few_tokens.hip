@@ -3,10 +3,12 @@
 //
 // The weights of the chosen experts are read once and everything else is
 // small, so streaming them is the bound.  A wave owns 16 rows of one expert's
-// matrix: the A operand of v_mfma_f32_16x16x32_bf16 (weights in 8 or 4 bits are
-// widened in registers, exactly); the expert's tokens are the B operand, from
-// LDS.  The order of the reduction is free, so a lane takes whichever
-// consecutive elements its 16 bytes hold and reads the same ones of x.
+// matrix: the A operand of v_mfma_f32_16x16x32_bf16; the expert's tokens are the
+// B operand, from LDS.  The order of the reduction is free, so a lane takes
+// whichever consecutive elements its 16 bytes hold and reads the same ones of x.
+// Weights in 8 or 4 bits are widened in registers, exactly where bf16 holds a
+// value of that size: below 2^-126 in its steps of 2^-133, above 3.39e38 as
+// infinite.
 //
 // h = silu(gate) up is rounded to bf16 between the two products, as the grouped
 // GEMM's SwiGLU epilogue does, so decoding and training see the same values.
@@ -49,9 +51,10 @@ __host__ __device__ constexpr int scale_region(int K, int wt, int waves, int spl
 // 1 token, 4 experts of 2880 x 2880 bf16 (92 KB tiles): 24.8 / 22.8, 26.8 / 14.4,
 // 22.4 / 15.2, 22.5 / 13.2; 7 tokens, 4096 x 2048 MXFP4 (32 and 16 KB): 49 / 27,
 // 47 / 31, 58 / 48, 95 / 88; 64 tokens, the same in bf16 (131 and 65 KB): 551 / 307,
-// 570 / 281, 558 / 291, 604 / 320.  The layer, where 256 or 512 waves are asked for
-// whatever the stream: 24 tokens on 2 of 60 MXFP4 experts of 2016 x 1504 (16 and 12
-// KB) 43.2 and 46.3, 16 on 3 of 8 MXFP8 of 1056 x 800 (17 and 13 KB) 20.6 and 19.7.
+// 570 / 281, 558 / 291, 604 / 320 (there the rule's 4 and 4 are 1 and 4% from the
+// best).  The layer, where 256 or 512 waves are asked for whatever the stream: 24
+// tokens on 2 of 60 MXFP4 experts of 2016 x 1504 (16 and 12 KB) 43.2 and 46.3, 16 on 3
+// of 8 MXFP8 of 1056 x 800 (17 and 13 KB) 20.6 and 19.7.
 // The number of tokens does not enter, here or in where a stream starts (Path): a
 // token's sums do not depend on who shares its call.
 struct Layout {

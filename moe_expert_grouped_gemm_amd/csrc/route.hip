@@ -11,7 +11,7 @@
 //
 // What bounds it: launch and wave-reduction latency -- a token's choice is a
 // thousand vector instructions of a wave, so it is spread over the CUs; the
-// logits of 16384 tokens are 16 MB at most.
+// logits of 16384 tokens on 256 experts in fp32 are 16 MB.
 #include "route_device.hpp"
 
 namespace ptgg {
