@@ -101,6 +101,22 @@ typedef enum {
     PT_GATE_SIGMOID = 1      /* scores are sigmoid(logit) + bias, weights the sigmoids */
 } pt_gate;
 
+typedef enum {               /* of c = x w^T + bias, in pt_linear_*                     */
+    PT_ACT_NONE = 0,         /* c                                                      */
+    PT_ACT_SILU = 1,         /* c / (1 + e^-c)                                         */
+    PT_ACT_GELU = 2,         /* c (1 + erf(c / sqrt 2)) / 2                            */
+    PT_ACT_GELU_TANH = 3,    /* c (1 + tanh(sqrt(2 / pi) (c + 0.044715 c^3))) / 2      */
+    PT_ACT_RELU2 = 4,        /* max(c, 0)^2                                            */
+    PT_ACT_SWIGLU = 5        /* silu(c[:, :N/2]) * c[:, N/2:], N/2 columns             */
+} pt_act;
+
+typedef enum {               /* the gate of pt_block_norm_*                            */
+    PT_BLOCK_GATE_NONE = 0,  /* 1                                                      */
+    PT_BLOCK_GATE_COLS = 1,  /* bf16 [cols]: a factor per channel                      */
+    PT_BLOCK_GATE_ROWS = 2,  /* fp32 [rows]: a factor per token                        */
+    PT_BLOCK_GATE_FULL = 3   /* bf16 [rows, cols]                                      */
+} pt_block_gate;
+
 /* Largest expert count one call accepts. */
 #define PT_MAX_GROUPS 1024
 /* Most experts per token that the router chooses. */
@@ -723,6 +739,169 @@ int pt_moe_few_tokens(const void *x, const void *logits, const float *bias, cons
                       float scale, int weight_dtype, float swiglu_limit, void *workspace, size_t workspace_bytes,
                       void *stream);
 size_t pt_moe_few_tokens_workspace_size(int64_t T, int64_t E, int64_t H, int64_t I, int64_t k);
+
+/*
+ * Dense matrix product with bias, activation and residual in its epilogue (a
+ * shared expert, an attention projection, the router's logits): with
+ *     c = x . w^T + bias                                            (fp32)
+ *     out = act(c) + residual               rounded once to out's type
+ *  x        [M, K] bf16;  w [N, K] bf16, the [out, in] weight layout
+ *  bias     [N] bf16, or NULL
+ *  act      a pt_act; PT_ACT_SWIGLU takes c as [gate | up] halves, gate first,
+ *           and gives N/2 columns
+ *  residual [M, N] (SwiGLU: [M, N/2]) of out_dtype, or NULL; may be out itself
+ *  out      [M, N] (SwiGLU: [M, N/2]) of out_dtype: PT_BF16 or PT_FP32
+ *  c        [M, N] bf16: c rounded, kept for the backward, or NULL
+ *  swiglu_limit  as pt_grouped_gemm_fwd, with PT_ACT_SWIGLU (0 or infinity:
+ *           none; NaN: PT_ERR_INVALID_ARG); a gate or an up that is NaN stays NaN
+ *  workspace  pt_linear_workspace_size(PT_OP_FWD, M, N, K) bytes, 16-byte
+ *           aligned (0 bytes where the reduction is not cut)
+ * Deterministic: sums over K are fp32, cut in parts by a rule on M, N and K and
+ * added in order.  M = 0 writes nothing.
+ *  Requirements: N % 8 == 0 (SwiGLU: N % 16 == 0), K % 8 == 0, M <= 2^23, N and
+ *  K <= 2^17, M N and M K <= 2^38; x, w, bias, residual, out and c 16-byte
+ *  aligned.  Operands may exceed 2 GiB.
+ */
+int pt_linear_fwd(const void *x, const void *w, const void *bias, const void *residual, void *out, void *c, int64_t M,
+                  int64_t N, int64_t K, int act, int out_dtype, float swiglu_limit, void *workspace,
+                  size_t workspace_bytes, void *stream);
+
+/*
+ * Its data gradient, ended by the gradient of the activation that made x: with
+ * dh = dy . w in fp32,
+ *     dx = dh * act'(c) + add               rounded once to bf16
+ * where c are the sums that the forward of the product before this one kept,
+ * x = act(c).  With PT_ACT_NONE there is no c and dx = dh + add.
+ *  dy   [M, N] bf16;  w [N, K] bf16
+ *  c    [M, K] bf16; PT_ACT_SWIGLU: [M, 2K] as [gate | up];  NULL with PT_ACT_NONE
+ *  add  [M, K] bf16, or NULL (NULL with PT_ACT_SWIGLU): what reaches dx by another
+ *       path; may be dx itself
+ *  dx   [M, K] bf16; PT_ACT_SWIGLU: [M, 2K], the gradients of gates and ups
+ *  swiglu_limit  the forward's: a clamped gate or up has no gradient
+ *  workspace  pt_linear_workspace_size(PT_OP_DGRAD, M, N, K) bytes
+ *  Requirements as pt_linear_fwd.  The gradient of the residual is that of out.
+ */
+int pt_linear_dgrad(const void *dy, const void *w, const void *c, const void *add, void *dx, int64_t M, int64_t N,
+                    int64_t K, int act, float swiglu_limit, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Its weight and bias gradients:
+ *     main_grad = (accumulate ? main_grad : 0) + dy^T . x            [N, K] fp32
+ *     dbias     = (accumulate ? dbias : 0) + sum over rows of dy     [N] fp32
+ *  x [M, K] bf16;  dy [M, N] bf16, the gradient of c;  dbias may be NULL
+ *  workspace  pt_linear_workspace_size(PT_OP_WGRAD, M, N, K) bytes
+ *  M = 0 writes zeros where it does not accumulate.  Sums over M are fp32, cut
+ *  in parts and added in order: deterministic.
+ *  Requirements as pt_linear_fwd; main_grad and dbias 16-byte aligned.
+ */
+int pt_linear_wgrad(const void *x, const void *dy, float *main_grad, float *dbias, int64_t M, int64_t N, int64_t K,
+                    int accumulate, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * The gradient of c alone, where no product follows the activation:
+ *     dc = dout * act'(c)                   rounded once to bf16
+ *  dout [M, N] bf16 (SwiGLU: [M, N/2]);  c and dc [M, N] bf16 (dc may be c
+ *  itself, or, but with SwiGLU, dout)
+ *  act  any but PT_ACT_NONE;  swiglu_limit and requirements as pt_linear_fwd
+ */
+int pt_linear_act_bwd(const void *dout, const void *c, void *dc, int64_t M, int64_t N, int act, float swiglu_limit,
+                      void *stream);
+/* Bytes of workspace; op PT_OP_FWD, PT_OP_DGRAD or PT_OP_WGRAD, M, N and K as the call's. */
+size_t pt_linear_workspace_size(int op, int64_t M, int64_t N, int64_t K);
+
+/*
+ * What lies between two blocks of a transformer: the norm after the block, its
+ * gate and scale, the residual stream, the norm before the next block.  Per row
+ *     u = x * rstd_post * post_weight       rstd_post = 1 / sqrt(mean(x^2) + eps)
+ *     h = residual_scale * residual + branch_scale * gate * u
+ *                                           rounded once to the stream's type
+ *     v = h * rstd_pre * pre_weight         rstd_pre = 1 / sqrt(mean(h^2) + eps)
+ *     y = bf16(v),  q = codes of v          (as pt_rmsnorm_fwd)
+ * all in fp32 but for the roundings named; rstd_pre is that of the rounded h.
+ *  x            [rows, cols] bf16: the block's output
+ *  residual     [rows, cols] of stream_dtype
+ *  post_weight  [cols] bf16, or NULL: no norm after the block, u = x
+ *  gate         as gate_kind (a pt_block_gate) says; NULL with PT_BLOCK_GATE_NONE
+ *  pre_weight   [cols] bf16, or NULL: no norm before the next block; y, q, scales
+ *               and rstd_pre are then NULL
+ *  residual_out [rows, cols] of stream_dtype: h (may be residual itself)
+ *  y            [rows, cols] bf16, or NULL where codes are asked for
+ *  q, scales    as pt_rmsnorm_fwd for code_dtype
+ *  rstd_post, rstd_pre  [rows] fp32 for the backward, or NULL
+ * Rows of zeros, NaN and infinities as pt_rmsnorm_fwd.
+ *  Requirements: cols % 8 == 0 (cols % 32 == 0 for MXFP8), cols <= 16384,
+ *  rows <= 2^23, eps >= 0; matrices, weights and gate 16-byte aligned (a gate per
+ *  row 4-byte).
+ */
+int pt_block_norm_fwd(const void *x, const void *residual, const void *post_weight, const void *gate,
+                      const void *pre_weight, void *residual_out, void *y, void *q, void *scales, float *rstd_post,
+                      float *rstd_pre, int64_t rows, int64_t cols, float eps, float branch_scale, float residual_scale,
+                      int gate_kind, int stream_dtype, int code_dtype, void *stream);
+
+/*
+ * Its backward, the codes taken as v itself.  With xhat = x * rstd_post, shat =
+ * s * rstd_pre and g = dy * pre_weight, for each row
+ *     ds        = dres + rstd_pre * (g - shat * mean(g * shat))      (fp32)
+ *     dresidual = residual_scale * ds
+ *     e         = branch_scale * gate * ds * post_weight
+ *     dx        = rstd_post * (e - xhat * mean(e * xhat))
+ *     dgate     = branch_scale * ds * xhat * post_weight, summed to the gate's shape
+ *     dpost     = sum over rows of branch_scale * gate * ds * xhat
+ *     dpre      = sum over rows of dy * shat
+ *  dy         [rows, cols] bf16 (NULL without pre_weight);  x and s the forward's
+ *             x and residual_out (s is not read without pre_weight)
+ *  dres       [rows, cols] of stream_dtype: the gradient that reaches the stream
+ *             past the next block, or NULL (not without pre_weight)
+ *  dx         [rows, cols] bf16;  dresidual [rows, cols] of stream_dtype (may be
+ *             dres itself)
+ *  dgate      fp32 [cols], fp32 [rows] or bf16 [rows, cols] by gate_kind, or NULL
+ *  dpost, dpre  [cols] fp32, or NULL
+ *  accumulate adds to dpost, dpre and a gate per channel's dgate; the others are
+ *             written
+ *  workspace  pt_block_norm_workspace_size(rows, cols) bytes, 16-byte aligned,
+ *             where one of those sums over rows is wanted; they are added in a
+ *             fixed order, so results are deterministic
+ *  The other arguments are the forward's.
+ */
+int pt_block_norm_bwd(const void *dy, const void *dres, const void *x, const void *s, const void *post_weight,
+                      const void *gate, const void *pre_weight, const float *rstd_post, const float *rstd_pre, void *dx,
+                      void *dresidual, void *dgate, float *dpost, float *dpre, int64_t rows, int64_t cols,
+                      float branch_scale, float residual_scale, int gate_kind, int stream_dtype, int accumulate,
+                      void *workspace, size_t workspace_bytes, void *stream);
+size_t pt_block_norm_workspace_size(int64_t rows, int64_t cols);
+
+/*
+ * The experts' rows back to their tokens:
+ *     out[t] = bf16( base[t] + sum over slots j of weights[t, j] * rows[row_of[t, j]] )
+ * added in fp32 in the slots' order.
+ *  rows     [M, H] bf16: the expert products' output, in pt_moe_route's row order
+ *  weights  [T, k] fp32, or NULL: all 1 (the gradient of the gather that made the
+ *           experts' operand)
+ *  row_of   [T, k] int32 as pt_moe_route gave it; a slot outside [0, M) adds nothing
+ *           and its weight is not read
+ *  base     [T, H] bf16: a shared expert's output, or NULL; may be out itself
+ *  out      [T, H] bf16
+ *  Requirements: H % 8 == 0, H <= 32768, k <= PT_MAX_TOPK, T <= 2^23, M < 2^31;
+ *  rows, base and out 16-byte aligned.
+ */
+int pt_moe_combine(const void *rows, const float *weights, const int32_t *row_of, const void *base, void *out, int64_t T,
+                   int64_t M, int64_t H, int64_t k, void *stream);
+
+/*
+ * Its gradients (that of base is dout):
+ *     drows[row_of[t, j]] = bf16( weights[t, j] * dout[t] )
+ *     dweights[t, j]      = sum over columns of dout[t] * rows[row_of[t, j]]   (fp32)
+ * Without weights and dweights it is the gather A[row_of[t, j]] = x[t] of the
+ * experts' operand, each row of x read once.
+ *  drows    [M, H] bf16, or NULL; rows that no slot names are left as they are.  A
+ *           row is named once, as pt_moe_route does: of two slots that name the
+ *           same row one is written
+ *  dweights [T, k] fp32, or NULL; 0 for a slot without a row
+ *  rows     [M, H] bf16: needed for dweights, else NULL
+ *  Requirements as pt_moe_combine; dout and drows 16-byte aligned.
+ */
+int pt_moe_combine_bwd(const void *dout, const void *rows, const float *weights, const int32_t *row_of, void *drows,
+                       float *dweights, int64_t T, int64_t M, int64_t H, int64_t k, void *stream);
 
 /*
  * Kernel configurations and tuning (the Primus-Turbo README, "What's New":

@@ -32,6 +32,10 @@ __all__ = [
     "pt_rmsnorm_fwd", "pt_rmsnorm_bwd", "pt_rmsnorm_workspace_size",
     "pt_moe_route", "pt_moe_route_bwd", "pt_moe_route_workspace_size",
     "pt_moe_few_tokens", "pt_moe_few_tokens_workspace_size",
+    "pt_linear_fwd", "pt_linear_dgrad", "pt_linear_wgrad", "pt_linear_act_bwd", "pt_linear_workspace_size",
+    "pt_block_norm_fwd", "pt_block_norm_bwd", "pt_block_norm_workspace_size", "pt_moe_combine", "pt_moe_combine_bwd",
+    "PT_ACT_NONE", "PT_ACT_SILU", "PT_ACT_GELU", "PT_ACT_GELU_TANH", "PT_ACT_RELU2", "PT_ACT_SWIGLU",
+    "PT_BLOCK_GATE_NONE", "PT_BLOCK_GATE_COLS", "PT_BLOCK_GATE_ROWS", "PT_BLOCK_GATE_FULL",
     "PT_FP32", "PT_GATE_SOFTMAX", "PT_GATE_SIGMOID", "PT_MAX_TOPK", "PT_FEW_TOKENS",
     "pt_grouped_gemm_workspace_size", "pt_read_error_flags", "pt_status_string", "pt_version",
 ]
@@ -44,6 +48,8 @@ PT_MAX_GROUPS = 1024
 PT_FP32 = 5
 PT_GATE_SOFTMAX, PT_GATE_SIGMOID = 0, 1
 PT_MAX_TOPK, PT_FEW_TOKENS = 16, 64
+PT_ACT_NONE, PT_ACT_SILU, PT_ACT_GELU, PT_ACT_GELU_TANH, PT_ACT_RELU2, PT_ACT_SWIGLU = 0, 1, 2, 3, 4, 5
+PT_BLOCK_GATE_NONE, PT_BLOCK_GATE_COLS, PT_BLOCK_GATE_ROWS, PT_BLOCK_GATE_FULL = 0, 1, 2, 3
 
 EXPORTS = (
     "pt_grouped_gemm_fwd", "pt_grouped_gemm_dgrad", "pt_grouped_gemm_dgrad_swiglu", "pt_grouped_gemm_wgrad",
@@ -54,6 +60,8 @@ EXPORTS = (
     "pt_rmsnorm_fwd", "pt_rmsnorm_bwd", "pt_rmsnorm_workspace_size",
     "pt_moe_route", "pt_moe_route_bwd", "pt_moe_route_workspace_size",
     "pt_moe_few_tokens", "pt_moe_few_tokens_workspace_size",
+    "pt_linear_fwd", "pt_linear_dgrad", "pt_linear_wgrad", "pt_linear_act_bwd", "pt_linear_workspace_size",
+    "pt_block_norm_fwd", "pt_block_norm_bwd", "pt_block_norm_workspace_size", "pt_moe_combine", "pt_moe_combine_bwd",
     "pt_grouped_gemm_workspace_size", "pt_read_error_flags", "pt_status_string", "pt_version",
 )
 
@@ -140,6 +148,26 @@ def load(require_gpu: bool = True):
                                     p, sz, p]
     L.pt_moe_few_tokens_workspace_size.restype = sz
     L.pt_moe_few_tokens_workspace_size.argtypes = [i64, i64, i64, i64, i64]
+    L.pt_linear_fwd.restype = i32
+    L.pt_linear_fwd.argtypes = [p, p, p, p, p, p, i64, i64, i64, i32, i32, f32, p, sz, p]
+    L.pt_linear_dgrad.restype = i32
+    L.pt_linear_dgrad.argtypes = [p, p, p, p, p, i64, i64, i64, i32, f32, p, sz, p]
+    L.pt_linear_wgrad.restype = i32
+    L.pt_linear_wgrad.argtypes = [p, p, p, p, i64, i64, i64, i32, p, sz, p]
+    L.pt_linear_act_bwd.restype = i32
+    L.pt_linear_act_bwd.argtypes = [p, p, p, i64, i64, i32, f32, p]
+    L.pt_linear_workspace_size.restype = sz
+    L.pt_linear_workspace_size.argtypes = [i32, i64, i64, i64]
+    L.pt_block_norm_fwd.restype = i32
+    L.pt_block_norm_fwd.argtypes = [p] * 11 + [i64, i64, f32, f32, f32, i32, i32, i32, p]
+    L.pt_block_norm_bwd.restype = i32
+    L.pt_block_norm_bwd.argtypes = [p] * 14 + [i64, i64, f32, f32, i32, i32, i32, p, sz, p]
+    L.pt_block_norm_workspace_size.restype = sz
+    L.pt_block_norm_workspace_size.argtypes = [i64, i64]
+    L.pt_moe_combine.restype = i32
+    L.pt_moe_combine.argtypes = [p, p, p, p, p, i64, i64, i64, i64, p]
+    L.pt_moe_combine_bwd.restype = i32
+    L.pt_moe_combine_bwd.argtypes = [p, p, p, p, p, p, i64, i64, i64, i64, p]
     L.pt_grouped_gemm_workspace_size.argtypes = [i32, i64, i64, i64, i64, i32]
     L.pt_read_error_flags.restype = i32
     L.pt_read_error_flags.argtypes = [p, p, ctypes.POINTER(ctypes.c_uint32)]
@@ -365,6 +393,74 @@ def pt_moe_few_tokens(x, logits, bias, w1, w1_scale, w2, w2_scale, out, topk_ids
 
 def pt_moe_few_tokens_workspace_size(T, E, H, I, k) -> int:
     return int(load(require_gpu=False).pt_moe_few_tokens_workspace_size(T, E, H, I, k))
+
+
+def pt_linear_fwd(x, w, bias, residual, out, c, M, N, K, act=PT_ACT_NONE, out_dtype=PT_BF16, workspace=None, stream=None,
+                  swiglu_limit=0.0):
+    L = load()
+    _check("pt_linear_fwd", L.pt_linear_fwd(
+        _ptr(x), _ptr(w), _ptr(bias), _ptr(residual), _ptr(out), _ptr(c), M, N, K, act, out_dtype, swiglu_limit,
+        _ptr(workspace), _nbytes(workspace), _stream(stream)))
+
+
+def pt_linear_dgrad(dy, w, c, add, dx, M, N, K, act=PT_ACT_NONE, workspace=None, stream=None, swiglu_limit=0.0):
+    L = load()
+    _check("pt_linear_dgrad", L.pt_linear_dgrad(
+        _ptr(dy), _ptr(w), _ptr(c), _ptr(add), _ptr(dx), M, N, K, act, swiglu_limit, _ptr(workspace),
+        _nbytes(workspace), _stream(stream)))
+
+
+def pt_linear_wgrad(x, dy, main_grad, dbias, M, N, K, accumulate=0, workspace=None, stream=None):
+    L = load()
+    _check("pt_linear_wgrad", L.pt_linear_wgrad(
+        _ptr(x), _ptr(dy), _ptr(main_grad), _ptr(dbias), M, N, K, accumulate, _ptr(workspace), _nbytes(workspace),
+        _stream(stream)))
+
+
+def pt_linear_act_bwd(dout, c, dc, M, N, act, stream=None, swiglu_limit=0.0):
+    L = load()
+    _check("pt_linear_act_bwd", L.pt_linear_act_bwd(
+        _ptr(dout), _ptr(c), _ptr(dc), M, N, act, swiglu_limit, _stream(stream)))
+
+
+def pt_linear_workspace_size(op, M, N, K) -> int:
+    return int(load(require_gpu=False).pt_linear_workspace_size(op, M, N, K))
+
+
+def pt_block_norm_fwd(x, residual, post_weight, gate, pre_weight, residual_out, y, q, scales, rstd_post, rstd_pre, rows,
+                      cols, eps, branch_scale=1.0, residual_scale=1.0, gate_kind=PT_BLOCK_GATE_NONE,
+                      stream_dtype=PT_BF16, code_dtype=PT_BF16, stream=None):
+    L = load()
+    _check("pt_block_norm_fwd", L.pt_block_norm_fwd(
+        _ptr(x), _ptr(residual), _ptr(post_weight), _ptr(gate), _ptr(pre_weight), _ptr(residual_out), _ptr(y), _ptr(q),
+        _ptr(scales), _ptr(rstd_post), _ptr(rstd_pre), rows, cols, eps, branch_scale, residual_scale, gate_kind,
+        stream_dtype, code_dtype, _stream(stream)))
+
+
+def pt_block_norm_bwd(dy, dres, x, s, post_weight, gate, pre_weight, rstd_post, rstd_pre, dx, dresidual, dgate, dpost,
+                      dpre, rows, cols, branch_scale=1.0, residual_scale=1.0, gate_kind=PT_BLOCK_GATE_NONE,
+                      stream_dtype=PT_BF16, accumulate=0, workspace=None, stream=None):
+    L = load()
+    _check("pt_block_norm_bwd", L.pt_block_norm_bwd(
+        _ptr(dy), _ptr(dres), _ptr(x), _ptr(s), _ptr(post_weight), _ptr(gate), _ptr(pre_weight), _ptr(rstd_post),
+        _ptr(rstd_pre), _ptr(dx), _ptr(dresidual), _ptr(dgate), _ptr(dpost), _ptr(dpre), rows, cols, branch_scale,
+        residual_scale, gate_kind, stream_dtype, accumulate, _ptr(workspace), _nbytes(workspace), _stream(stream)))
+
+
+def pt_block_norm_workspace_size(rows, cols) -> int:
+    return int(load(require_gpu=False).pt_block_norm_workspace_size(rows, cols))
+
+
+def pt_moe_combine(rows, weights, row_of, base, out, T, M, H, k, stream=None):
+    L = load()
+    _check("pt_moe_combine", L.pt_moe_combine(
+        _ptr(rows), _ptr(weights), _ptr(row_of), _ptr(base), _ptr(out), T, M, H, k, _stream(stream)))
+
+
+def pt_moe_combine_bwd(dout, rows, weights, row_of, drows, dweights, T, M, H, k, stream=None):
+    L = load()
+    _check("pt_moe_combine_bwd", L.pt_moe_combine_bwd(
+        _ptr(dout), _ptr(rows), _ptr(weights), _ptr(row_of), _ptr(drows), _ptr(dweights), T, M, H, k, _stream(stream)))
 
 
 def pt_set_gemm_config(config) -> int:
