@@ -17,6 +17,8 @@
 // and residual are applied to unrounded sums and the result is rounded once.
 // Where the tiles alone do not fill the chip the reduction is cut in parts
 // whose fp32 sums a second kernel adds in order and finishes.
+#include <utility>
+
 #include "dense.hpp"
 #include "pipeline.hpp"
 #include "rows.hpp"
@@ -28,20 +30,25 @@ namespace {
 template <int V>
 struct IC { static constexpr int value = V; };
 
+template <class F, int... I>
+__device__ __forceinline__ void unrolled(F &&f, std::integer_sequence<int, I...>)
+{
+    (f(IC<I>{}), ...);
+}
+template <int N, class F>
+__device__ __forceinline__ void unrolled(F &&f)
+{
+    unrolled((F &&)f, std::make_integer_sequence<int, N>{});
+}
+
+constexpr int kWideRows = 256;                // most rows of a tile
 constexpr int kStage = 64;                    // reduction values of a stage
 
 // ------------------------------------------------------------------ activations
-// e^x to about an ulp: the product x log2(e) in two parts, its whole part by
-// ldexp.  Past +-150 it is 0 or infinite (NaN becomes some number: the callers
-// multiply by their argument).
-__device__ __forceinline__ float exp_(float x)
-{
-    constexpr float kL = 1.44269502162933349609375f, kLow = 1.925963033500011e-8f;
-    x = __builtin_amdgcn_fmed3f(x, -150.0f, 150.0f);
-    const float n = __builtin_rintf(x * kL);
-    const float f = __builtin_fmaf(x, kLow, __builtin_fmaf(x, kL, -n));
-    return __builtin_ldexpf(__builtin_amdgcn_exp2f(f), (int)n);
-}
+// e^x by the hardware's 2^x.  The rounding of x log2(e) makes it |x| 2^-24 off,
+// relative: in what it is used for, sigmoids of c times c, less than an ulp of
+// |c| + 1.  Past the type's range it is 0 or infinite, of a NaN a NaN.
+__device__ __forceinline__ float exp_(float x) { return __builtin_amdgcn_exp2f(1.44269502162933349609375f * x); }
 __device__ __forceinline__ float sigmoid_(float x) { return __builtin_amdgcn_rcpf(1.0f + exp_(-x)); }
 
 constexpr float kSqrtHalf = 0.707106769084930419921875f;
@@ -84,54 +91,50 @@ __device__ __forceinline__ float act_slope(float c, int act)
 }
 
 // SwiGLU's clamp: a gate at most lim, an up within [-lim, lim]; NaN stays.
-__device__ __forceinline__ float glu_of(float g, float u, float lim)
+__device__ __forceinline__ void glu8(float (&g)[8], float (&u)[8], float lim)
 {
-    g = g > lim ? lim : g;
-    u = u > lim ? lim : u < -lim ? -lim : u;
-    return g * sigmoid_(g) * u;
-}
-__device__ __forceinline__ void glu_slope(float g0, float u0, float lim, float d, float &dg, float &du)
-{
-    const float g = g0 > lim ? lim : g0, u = u0 > lim ? lim : u0 < -lim ? -lim : u0;
-    const float s = sigmoid_(g);
-    dg = g0 > lim ? 0.0f : d * u * (s * (1.0f + g * (1.0f - s)));
-    du = __builtin_fabsf(u0) > lim ? 0.0f : d * (g * s);
-    if (g != g) du = dg;                 // a NaN gate makes both NaN, also where the sigmoid dropped it
-}
-
-// ------------------------------------------------------------------ finish
-// Eight neighbouring sums v of row m and, for kFinFwdGlu, the eight ups u that
-// belong to them; n: v's first column of the product.  Sums are fp32 until the
-// one rounding of each output.
-__device__ __forceinline__ void store8(const FinishParams &p, int64_t at, const float (&v)[8])
-{
-    if (p.f32) store_stream<true, false>(p.out, at, v);
-    else store_stream<false, false>(p.out, at, v);
-}
-
-__device__ __forceinline__ void add_row8(const uint16_t *b, float (&v)[8])
-{
-    float f[8];
-    unpack8(*(const uintx4 *)b, f);
+    if (lim < __builtin_huge_valf()) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] += f[i];
-}
-
-__device__ __forceinline__ void add_residual8(const FinishParams &p, int64_t at, float (&v)[8])
-{
-    if (!p.residual) return;
-    float f[8];
-    if (p.f32) load_stream<true, false>(p.residual, at, f);
-    else load_stream<false, false>(p.residual, at, f);
+        for (int i = 0; i < 8; ++i) {
+            g[i] = g[i] > lim ? lim : g[i];
+            u[i] = u[i] > lim ? lim : u[i] < -lim ? -lim : u[i];
+        }
+    }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] += f[i];
+    for (int i = 0; i < 8; ++i) g[i] = g[i] * sigmoid_(g[i]) * u[i];
+}
+// g, u: the saved gates and ups, then their gradients for d, those of the products
+__device__ __forceinline__ void glu_slope8(float (&g)[8], float (&u)[8], const float (&d)[8], float lim)
+{
+    uint32_t shut = 0;                   // bits of gates and ups that the clamp holds: no gradient into them
+    if (lim < __builtin_huge_valf()) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            shut |= (g[i] > lim ? 1u : 0u) << i | (__builtin_fabsf(u[i]) > lim ? 1u : 0u) << (8 + i);
+            g[i] = g[i] > lim ? lim : g[i];
+            u[i] = u[i] > lim ? lim : u[i] < -lim ? -lim : u[i];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float s = sigmoid_(g[i]), dg = d[i] * u[i] * (s * (1.0f + g[i] * (1.0f - s)));
+        u[i] = d[i] * (g[i] * s);
+        g[i] = dg;
+    }
+    if (shut) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (shut >> i & 1) g[i] = 0.0f;
+            if (shut >> (8 + i) & 1) u[i] = 0.0f;
+        }
+    }
 }
 
 __device__ __forceinline__ void act8(float (&v)[8], int act)
 {
     switch (act) {                       // one branch for the eight
-#define PTGG_ACT(A)                                       \
-    case A:                                               \
+#define PTGG_ACT(A)                                                           \
+    case A:                                                                   \
         _Pragma("unroll") for (int i = 0; i < 8; ++i) v[i] = act_of(v[i], A); \
         break;
         PTGG_ACT(kActSilu)
@@ -146,8 +149,8 @@ __device__ __forceinline__ void act8(float (&v)[8], int act)
 __device__ __forceinline__ void slope8(float (&v)[8], const float (&c)[8], int act)
 {
     switch (act) {
-#define PTGG_ACT(A)                                       \
-    case A:                                               \
+#define PTGG_ACT(A)                                                               \
+    case A:                                                                       \
         _Pragma("unroll") for (int i = 0; i < 8; ++i) v[i] *= act_slope(c[i], A); \
         break;
         PTGG_ACT(kActSilu)
@@ -159,52 +162,177 @@ __device__ __forceinline__ void slope8(float (&v)[8], const float (&c)[8], int a
     }
 }
 
-__device__ __forceinline__ void finish8(const FinishParams &p, int64_t m, int64_t n, float (&v)[8], float (&u)[8])
+// ------------------------------------------------------------------ finish
+// What becomes of eight neighbouring sums of a row.  Sums are fp32 until the one
+// rounding of each output.  v: the sums from some column of the product on, u,
+// for kFinFwdGlu: those of the ups, N / 2 columns on; afterwards the outputs.
+struct Extra {
+    uintx4 r[2];                          // residual, as it lies in memory (bf16: r[0])
+    uintx4 c[2];                          // kFinGrad*: the saved sums, of gates and ups
+};
+struct Saved {
+    uintx4 v, u;                          // kFinFwd*: the sums with bias, in bf16
+};
+
+template <int FIN>
+__device__ __forceinline__ Saved finish8(const FinishParams &p, const float (&bias)[8], const float (&bias_u)[8], const Extra &x,
+                                         float (&v)[8], float (&u)[8])
 {
-    const int64_t at = m * p.ldo + n;
-    if (p.finish == kFinFwd) {
-        if (p.bias) add_row8(p.bias + n, v);
-        if (p.save) *(uintx4 *)(p.save + m * p.N + n) = pack8(v);
-        act8(v, p.act);
-        add_residual8(p, at, v);
-        store8(p, at, v);
-    } else if (p.finish == kFinFwdGlu) {
-        const int64_t I = p.N >> 1;
-        if (p.bias) {
-            add_row8(p.bias + n, v);
-            add_row8(p.bias + I + n, u);
+    Saved saved = {};
+    if constexpr (FIN == kFinFwd || FIN == kFinFwdGlu) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] += bias[i];
+        if (FIN == kFinFwdGlu) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) u[i] += bias_u[i];
         }
         if (p.save) {
-            *(uintx4 *)(p.save + m * p.N + n) = pack8(v);
-            *(uintx4 *)(p.save + m * p.N + I + n) = pack8(u);
+            saved.v = pack8(v);
+            if (FIN == kFinFwdGlu) saved.u = pack8(u);
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = glu_of(v[i], u[i], p.limit);
-        add_residual8(p, at, v);
-        store8(p, at, v);
-    } else if (p.finish == kFinGrad) {
-        if (p.c) {
-            float c[8];
-            unpack8(*(const uintx4 *)(p.c + at), c);
-            slope8(v, c, p.act);
-        }
-        add_residual8(p, at, v);
-        store8(p, at, v);
+        if (FIN == kFinFwdGlu) glu8(v, u, p.limit);
+        else act8(v, p.act);
+    } else if constexpr (FIN == kFinGrad) {
+        float c[8];
+        unpack8(x.c[0], c);
+        slope8(v, c, p.act);
     } else {
-        const int64_t I = p.N;           // ldo is 2 N
-        float g[8];
-        unpack8(*(const uintx4 *)(p.c + at), g);
-        unpack8(*(const uintx4 *)(p.c + at + I), u);
+        float g[8], w[8];
+        unpack8(x.c[0], g);
+        unpack8(x.c[1], w);
+        glu_slope8(g, w, v, p.limit);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) glu_slope(g[i], u[i], p.limit, v[i], g[i], u[i]);
-        store8(p, at, g);
-        store8(p, at + I, u);
+        for (int i = 0; i < 8; ++i) v[i] = g[i], u[i] = w[i];
+    }
+    if (FIN != kFinGradGlu && p.residual) {
+        float f[8];
+        if (p.f32) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = bits_f32(x.r[0][i]), f[4 + i] = bits_f32(x.r[1][i]);
+        } else {
+            unpack8(x.r[0], f);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] += f[i];
+    }
+    return saved;
+}
+
+template <int FIN>
+__device__ __forceinline__ void load_bias8(const FinishParams &p, int64_t n, float (&bias)[8], float (&bias_u)[8])
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i) bias[i] = bias_u[i] = 0.0f;
+    if ((FIN == kFinFwd || FIN == kFinFwdGlu) && p.bias) {
+        unpack8(*(const uintx4 *)(p.bias + n), bias);
+        if (FIN == kFinFwdGlu) unpack8(*(const uintx4 *)(p.bias + (p.N >> 1) + n), bias_u);
     }
 }
 
-// ------------------------------------------------------------------ operands
-__device__ __forceinline__ uint32_t clip_bytes(int64_t left) { return left <= 0 ? 0u : left > 0x7FFFFFFF ? 0x7FFFFFFFu : (uint32_t)left; }
+// One row, from its sums to memory.
+template <int FIN>
+__device__ __forceinline__ void finish_row(const FinishParams &p, int64_t m, int64_t n, float (&v)[8], float (&u)[8])
+{
+    const int64_t at = m * p.ldo + n;
+    float bias[8], bias_u[8];
+    load_bias8<FIN>(p, n, bias, bias_u);
+    Extra x = {};
+    if (FIN != kFinGradGlu && p.residual) {
+        if (p.f32) {
+            x.r[0] = *(const uintx4 *)((const float *)p.residual + at);
+            x.r[1] = *(const uintx4 *)((const float *)p.residual + at + 4);
+        } else {
+            x.r[0] = *(const uintx4 *)((const uint16_t *)p.residual + at);
+        }
+    }
+    if ((FIN == kFinGrad && p.c) || FIN == kFinGradGlu) x.c[0] = *(const uintx4 *)(p.c + at);
+    if (FIN == kFinGradGlu) x.c[1] = *(const uintx4 *)(p.c + at + p.N);
+    const Saved s = finish8<FIN>(p, bias, bias_u, x, v, u);
+    if ((FIN == kFinFwd || FIN == kFinFwdGlu) && p.save) {
+        *(uintx4 *)(p.save + m * p.N + n) = s.v;
+        if (FIN == kFinFwdGlu) *(uintx4 *)(p.save + m * p.N + (p.N >> 1) + n) = s.u;
+    }
+    if (p.f32) store_stream<true, false>(p.out, at, v);
+    else store_stream<false, false>(p.out, at, v);
+    if (FIN == kFinGradGlu) store_stream<false, false>(p.out, at + p.N, u);
+}
 
+// 16 bytes of a buffer at `base`; at or past `bytes` zeros are read and nothing is
+// written.  Plain functions: see dma16.
+__device__ __forceinline__ uintx4 buf_load(const void *base, uint32_t bytes, uint32_t voff, uint32_t soff)
+{
+    return __builtin_bit_cast(uintx4, __builtin_amdgcn_raw_buffer_load_b128(make_rsrc(base, bytes), voff, soff, 0));
+}
+__device__ __forceinline__ void buf_store(uintx4 v, const void *base, uint32_t bytes, uint32_t voff, uint32_t soff)
+{
+    typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), make_rsrc(base, bytes), voff, soff, 0);
+}
+
+// Rows of a wave from row m0 on, each lane at its 8 columns.  Loads and stores
+// have no branch around them -- what is not there has a bound of 0 -- so that the
+// wait for a row's loads is a count that leaves the stores in flight (with a
+// branch it was for every store before: 1000 cycles a row).
+template <int FIN>
+struct FinishRows {
+    static constexpr bool FWD = FIN == kFinFwd || FIN == kFinFwdGlu;
+    const FinishParams &p;
+    const uint8_t *out, *res, *sv, *cs;
+    uint32_t out_b, res_b, sv_b, cs_b;    // bounds
+    uint32_t vo, vs;                      // this lane's offsets in out (and residual and c) and in save
+    uint32_t ldo_b, lds_b;                // bytes of a row
+    uint32_t far_o, far_s;                // from the gates' columns to the ups'
+    uint32_t hi;                          // from the first 16 bytes of 8 outputs to the second, or out of bounds
+    float bias[8], bias_u[8];
+
+    __device__ __forceinline__ FinishRows(const FinishParams &f, int64_t m0, int64_t M, int r0, int64_t n, bool live) : p(f)
+    {
+        const int rows = (int)min(M - m0, (int64_t)kWideRows);
+        const uint32_t size = f.f32 ? 4 : 2;
+        ldo_b = (uint32_t)f.ldo * size;
+        lds_b = (uint32_t)f.N * 2;
+        out = (const uint8_t *)f.out + m0 * ldo_b;
+        out_b = rows > 0 ? rows * ldo_b : 0;
+        res = (const uint8_t *)f.residual + m0 * ldo_b;
+        res_b = f.residual ? out_b : 0;
+        sv = (const uint8_t *)f.save + m0 * lds_b;
+        sv_b = f.save && rows > 0 ? rows * lds_b : 0;
+        cs = (const uint8_t *)f.c + m0 * ldo_b;
+        cs_b = f.c ? out_b : 0;
+        vo = live ? r0 * ldo_b + (uint32_t)n * size : kOOB;
+        vs = live ? r0 * lds_b + (uint32_t)n * 2 : kOOB;
+        far_o = (uint32_t)f.N * 2;
+        far_s = (uint32_t)f.N;            // N / 2 columns
+        hi = f.f32 ? 16 : kOOB;
+        load_bias8<FIN>(f, live ? n : 0, bias, bias_u);
+    }
+    // `row` rows after this lane's first
+    __device__ __forceinline__ void fetch(Extra &x, uint32_t row) const
+    {
+        const uint32_t s = row * ldo_b;
+        if (FIN != kFinGradGlu) {
+            x.r[0] = buf_load(res, res_b, vo, s);
+            x.r[1] = buf_load(res, res_b, vo | (hi & kOOB), s + (hi & 16));
+        }
+        if (!FWD) x.c[0] = buf_load(cs, cs_b, vo, s);
+        if (FIN == kFinGradGlu) x.c[1] = buf_load(cs, cs_b, vo, s + far_o);
+    }
+    __device__ __forceinline__ void store(const Extra &x, uint32_t row, float (&v)[8], float (&u)[8]) const
+    {
+        const Saved sv8 = finish8<FIN>(p, bias, bias_u, x, v, u);
+        const uint32_t s = row * ldo_b;
+        if (FWD) buf_store(sv8.v, sv, sv_b, vs, row * lds_b);
+        if (FIN == kFinFwdGlu) buf_store(sv8.u, sv, sv_b, vs, row * lds_b + far_s);
+        uintx4 a, b = {f32_bits(v[4]), f32_bits(v[5]), f32_bits(v[6]), f32_bits(v[7])};
+        if (p.f32) a = uintx4{f32_bits(v[0]), f32_bits(v[1]), f32_bits(v[2]), f32_bits(v[3])};
+        else a = pack8(v);
+        buf_store(a, out, out_b, vo, s);
+        if (FWD) buf_store(b, out, out_b, vo | (hi & kOOB), s + (hi & 16));
+        if (FIN == kFinGradGlu) buf_store(pack8(u), out, out_b, vo, s + far_o);
+    }
+};
+
+// ------------------------------------------------------------------ operands
 // Chunk swizzles of a stage in LDS.  Along the reduction (rows of 128 bytes):
 // the 16 lanes of a ds_read_b128 pass, reading one chunk of 16 consecutive
 // rows, cover all banks.  Across it (rows of CPR chunks): the four rows of a
@@ -217,69 +345,95 @@ __device__ __forceinline__ int across(int k, int c)
 }
 
 // One operand of a tile: R rows (ALONG) or columns (!ALONG) of a stage, loaded
-// by NT threads, 16 bytes each.  The base moves on by a stage with every
-// issue, so that offsets stay small whatever the operand's size; loads at or
-// past `left` bytes read zeros.  Along the reduction the two halves of the
-// rows may lie apart (SwiGLU's gates and ups).
-template <bool ALONG, int R, int NT>
+// by NT threads, 16 bytes each.  The base moves on with every stage, so that
+// offsets and bounds stay small whatever the operand's size; loads at or past
+// the bound read zeros.
+//
+// PAIR > 0: the rows come in pairs of groups of PAIR, a wave's columns, of which
+// the second is taken from base[1]: with SwiGLU the ups of the first's gates.
+template <bool ALONG, int R, int NT, int PAIR>
 struct Operand {
     static constexpr int NL = R * 128 / 16 / NT;
     static constexpr int CPR = ALONG ? 8 : R / 8;          // 16-byte chunks of an LDS row
     static constexpr int RPL = NT / CPR;                   // LDS rows per load
-    static constexpr int HALVES = ALONG && NL >= 2 ? 2 : 1;
+    static constexpr int HALVES = PAIR >= RPL ? 2 : 1;
     static_assert(NL >= 1 && NT % CPR == 0 && RPL % 4 == 0, "loads of a stage");
     const uint8_t *base[HALVES];
-    int64_t left[HALVES];
+    uint32_t bytes[HALVES];                                // of the stage from its base
     int64_t step;
-    uint32_t voff, rstep;
-    int k;                                                 // this lane's first reduction value, ALONG
+    uint32_t voff, rstep, pstep;                           // bytes from load to load, and from pair to pair
+    int k;                                                 // ALONG: this lane's first reduction value
+    int klen, k0;                                          // reduction values, and those before the stage
+    uint32_t pitch, width;                                 // !ALONG: bytes of a row, and of its valid columns
 
-    // rows0, rows1: valid rows of the halves (ALONG); cols: valid columns (!ALONG)
-    __device__ __forceinline__ void init(const uint16_t *p0, const uint16_t *p1, int rows0, int rows1, int64_t ld,
-                                         int64_t klen, int64_t cols)
+    // rows0, rows1: valid rows from p0 and p1 (ALONG); pair: rows of base[0] from pair to pair; cols: valid columns (!ALONG)
+    __device__ __forceinline__ void init(const uint16_t *p0, const uint16_t *p1, int rows0, int rows1, int pair, int64_t ld,
+                                         int klen_, int64_t cols)
     {
         const int t = threadIdx.x, row = t / CPR;
         base[0] = (const uint8_t *)p0;
         rstep = (uint32_t)(RPL * ld * 2);
+        pstep = (uint32_t)(pair * ld * 2);
+        klen = klen_;
+        k0 = 0;
         if constexpr (ALONG) {
+            // up to the stage's end in the last row: what lies past klen there is left to the lanes (lane_offset), and
+            // a row after it starts at or past the bound
             const int chunk = along(row, t % CPR);
-            left[0] = rows0 > 0 ? ((rows0 - 1) * ld + klen) * 2 : 0;
+            const int64_t last = min(ld, (int64_t)kStage);
+            bytes[0] = rows0 > 0 ? (uint32_t)((rows0 - 1) * ld + last) * 2 : 0;
             voff = (uint32_t)(row * ld * 2) + chunk * 16;
             if constexpr (HALVES == 2) {
                 base[1] = (const uint8_t *)p1;
-                left[1] = rows1 > 0 ? ((rows1 - 1) * ld + klen) * 2 : 0;
-            } else if (R == 32) {
-                // one load takes both halves, which lie at most 32 rows apart
-                const int64_t apart = (p1 - p0) * 2;
-                if (rows1 > 0) left[0] = apart + ((rows1 - 1) * ld + klen) * 2;
-                if (row >= R / 2) voff = (uint32_t)(apart + (row - R / 2) * ld * 2) + chunk * 16;
+                bytes[1] = rows1 > 0 ? (uint32_t)((rows1 - 1) * ld + last) * 2 : 0;
+            } else if (PAIR > 0) {
+                // one load takes both groups, which lie at most 32 rows apart
+                static_assert(PAIR == 0 || 2 * PAIR == R || PAIR >= RPL, "a pair in one load");
+                const int64_t apart = p1 - p0;
+                if (rows1 > 0) bytes[0] = (uint32_t)(apart + (rows1 - 1) * ld + last) * 2;
+                if (row >= PAIR) voff = (uint32_t)(apart + (row - PAIR) * ld) * 2 + chunk * 16;
             }
             step = kStage * 2;
             k = chunk * 8;
         } else {
             const int chunk = across<CPR>(row, t % CPR);
-            left[0] = klen > 0 ? ((klen - 1) * ld + cols) * 2 : 0;
-            voff = (uint32_t)(row * ld * 2) + (uint32_t)min((int64_t)chunk * 8, cols - 8) * 2;
+            pitch = (uint32_t)ld * 2;
+            width = (uint32_t)min(cols, (int64_t)R) * 2;
+            voff = row * pitch + (uint32_t)min((int64_t)chunk * 8, cols - 8) * 2;
             step = kStage * ld * 2;
             k = 0;
+            bound();
         }
     }
-    // Stage at reduction value k0 of klen into the slot at `lds`.
-    __device__ __forceinline__ void issue(uint8_t *lds, int k0, int klen, int wave)
+    __device__ __forceinline__ void bound()
     {
-        uint32_t v = voff;
-        if (ALONG) v = k0 + k < klen ? voff : kOOB;
-        uint8_t *d = lds + wave * kWave * 16;
-#pragma unroll
-        for (int i = 0; i < NL; ++i) {
-            const int h = HALVES == 2 && i >= NL / 2;
-            dma16(base[h], clip_bytes(left[h]), d + i * NT * 16, v, (uint32_t)(h ? i - NL / 2 : i) * rstep);
+        if constexpr (!ALONG) {
+            const int rows = min(klen - k0, kStage);
+            bytes[0] = rows > 0 ? (uint32_t)(rows - 1) * pitch + width : 0;
         }
+    }
+    // This lane's offset in the stage, the same for all its loads.
+    __device__ __forceinline__ uint32_t lane_offset() const { return !ALONG || k0 + k < klen ? voff : kOOB; }
+    // One of the stage's loads into the slot at `lds`, and the step to the next stage after the last.
+    __device__ __forceinline__ void issue_one(uint8_t *lds, int i, uint32_t v, int wave) const
+    {
+        constexpr int LPG = HALVES == 2 ? PAIR / RPL : NL;           // loads of a group
+        const int q = i / LPG, h = HALVES == 2 ? q & 1 : 0;
+        dma16(base[h], bytes[h], lds + wave * kWave * 16 + i * NT * 16, v, (HALVES == 2 ? (q >> 1) * pstep : 0u) + (i % LPG) * rstep);
+    }
+    __device__ __forceinline__ void advance()
+    {
 #pragma unroll
-        for (int h = 0; h < HALVES; ++h) {
-            base[h] += step;
-            left[h] -= step;
-        }
+        for (int h = 0; h < HALVES; ++h) base[h] += step;
+        k0 += kStage;
+        bound();
+    }
+    __device__ __forceinline__ void issue(uint8_t *lds, int wave)
+    {
+        const uint32_t v = lane_offset();
+#pragma unroll
+        for (int i = 0; i < NL; ++i) issue_one(lds, i, v, wave);
+        advance();
     }
 };
 
@@ -307,25 +461,19 @@ __device__ __forceinline__ uint32_t frag_base(int first)
 
 template <bool ALONG, int R, int NB>
 struct Frags {
-    // across: one address per block, since the swizzle moves chunks of 32 bytes
-    // among 64 columns
-    static constexpr int NA = ALONG ? 1 : NB;
-    uint32_t at[NA];
-    __device__ __forceinline__ void init(uint32_t lds, int first)
-    {
-#pragma unroll
-        for (int i = 0; i < NA; ++i) at[i] = lds + frag_base<ALONG, R>(first + 32 * i);
-    }
+    uint32_t at;
+    __device__ __forceinline__ void init(uint32_t lds, int first) { at = lds + frag_base<ALONG, R>(first); }
     template <int KS>
     __device__ __forceinline__ void read(uint32_t slot, bf16x8 (&f)[NB], IC<KS>) const
     {
         if constexpr (ALONG) {
-            read_along<0>((at[0] + slot) ^ (uint32_t)(KS << 5), f);
+            read_along<0>((at + slot) ^ (uint32_t)(KS << 5), f);
         } else {
             constexpr int O = KS * 16 * R * 2;
 #pragma unroll
             for (int i = 0; i < NB; ++i) {
-                const uint32_t a = at[i] + slot;
+                // a block's 64 bytes: the rows' swizzle moves whole ones
+                const uint32_t a = (at + slot) ^ (uint32_t)(i << 6);
                 const uintx2 lo = read_tr<O>(a), hi = read_tr<O + 4 * R * 2>(a);
                 f[i] = __builtin_bit_cast(bf16x8, uintx4{lo[0], lo[1], hi[0], hi[1]});
             }
@@ -362,6 +510,10 @@ __device__ __forceinline__ void pin_frags(bf16x8 (&a)[NA], bf16x8 (&b)[NB])
 }
 
 // ------------------------------------------------------------------ kernel
+// Bytes of a row of C fp32 sums in LDS: 16 more, so that rows start on other banks.
+template <int C>
+constexpr int wave_pitch() { return C * 4 + 16; }
+
 // Tile TM x TN by WM x WN waves, times WK that share a stage's four steps of
 // the reduction; NS slots of the ring.
 template <int TM, int TN, int WM, int WN, int WK, int NS>
@@ -369,11 +521,10 @@ struct Shape {
     static constexpr int NT = kWave * WM * WN * WK;
     static constexpr int MI = TM / WM / 32, NJ = TN / WN / 32;
     static constexpr int SLOTA = TM * 128, SLOTB = TN * 128, SLOT = SLOTA + SLOTB, RING = NS * SLOT;
-    static constexpr int PITCH = TN * 4 + 16;             // bytes of an fp32 row of the tile in LDS
-    static constexpr int ER = TM * PITCH <= (96 << 10) ? TM : TM / 2;   // rows of the tile at a time
-    static constexpr int LDS = RING > ER * PITCH ? RING : ER * PITCH;
-    static constexpr int WGS = LDS * 2 <= (160 << 10) ? 2 : 1;    // workgroups on a CU
-    static_assert(LDS <= (160 << 10) && ER % (TM / WM) == 0, "LDS of a tile");
+    static constexpr int EPI = 32 * wave_pitch<NJ * 32>() * (WK > 1 ? MI * WK : 1);      // a wave's LDS in the epilogue
+    static constexpr int EPIS = WK > 1 ? EPI : EPI * WM * WN;
+    static constexpr int LDS = RING > EPIS ? RING : EPIS;
+    static_assert(LDS <= (160 << 10) && (WK == 1 || WM * WN == 1), "LDS of a tile");
 };
 
 // Logical workgroup number: consecutive ones share an XCD and its L2.
@@ -382,6 +533,164 @@ __device__ __forceinline__ uint32_t xcd_order()
     const uint32_t n = gridDim.x, b = blockIdx.x, q = n / 8, r = n % 8, x = b % 8;
     return x * q + min(x, r) + b / 8;
 }
+
+// A wave's sums finished: 32 rows at a time go through the wave's own part of LDS
+// in fp32, so that lanes hold 8 neighbouring columns and a row leaves in whole
+// lines; nothing waits for another wave.  Lane l holds of a block of 32 x 32 row
+// l % 32 and columns (r / 4) 8 + (l / 32) 4 + r % 4, of one of 16 x 16 row l % 16
+// and columns (l / 16) 4 + r.  With SwiGLU the wave's first C / 2
+// columns are gates, the others their ups.  WK waves hold sums of the same outputs:
+// they meet in LDS, where each finishes its share of the rows.
+template <int PITCH, int MI, int NJ>
+__device__ __forceinline__ void put_rows(const floatx16 (&acc)[MI][NJ], int i, uint8_t *to)
+{
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            *(floatx4 *)(to + (lane & 31) * PITCH + (j * 32 + q * 8 + (lane >> 5) * 4) * 4) =
+                floatx4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+}
+template <int PITCH, int MI, int NJ>
+__device__ __forceinline__ void put_rows(const floatx4 (&acc)[MI][NJ], int i, uint8_t *to)
+{
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+            *(floatx4 *)(to + (h * 16 + (lane & 15)) * PITCH + (j * 16 + (lane >> 4) * 4) * 4) = acc[2 * i + h][j];
+}
+
+template <int FIN, int MI, int NJ, int WK, class Acc>
+__device__ __forceinline__ void finish_wave_as(const LinearParams &p, const Acc &acc, uint8_t *lds, int wk, int64_t m0,
+                                               int64_t n0, int64_t split)
+{
+    constexpr int C = NJ * 32, PITCH = wave_pitch<C>();
+    constexpr bool GLU = FIN == kFinFwdGlu;
+    constexpr int GROUPS = C / (GLU ? 16 : 8), RPI = 64 / GROUPS;      // lanes of a row, rows of an instruction
+    constexpr int ROWS = WK > 1 ? MI * 32 / WK : 32, ITS = (ROWS + RPI - 1) / RPI;
+    const int lane = threadIdx.x & 63, g = lane % GROUPS, r0 = lane / GROUPS;
+    const int64_t n = n0 + g * 8, ncols = GLU ? p.N >> 1 : p.N;
+    auto get = [&](const uint8_t *src, float (&v)[8]) {
+#pragma unroll
+        for (int w = 0; w < WK; ++w) {
+            const floatx4 a = *(const floatx4 *)(src + w * MI * 32 * PITCH), b = *(const floatx4 *)(src + w * MI * 32 * PITCH + 16);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                v[x] = w ? v[x] + a[x] : a[x];
+                v[4 + x] = w ? v[4 + x] + b[x] : b[x];
+            }
+        }
+    };
+    // rows of LDS from `from` on; the next row's loads go out before one is worked on.  Loops, not copies: a wide tile's
+    // all unrolled were 350 KB of code that each workgroup had to fetch
+    auto share = [&](auto &&put_row, int from) {
+        const uint8_t *src = lds + (from + r0) * PITCH + g * 32;
+        float v[8], u[8], vn[8], un[8];
+        get(src, v);
+        if (GLU) get(src + C / 2 * 4, u);
+#pragma unroll 1
+        for (int it = 0; it < ITS; ++it) {
+            if (it + 1 < ITS) src += RPI * PITCH;
+            get(src, vn);
+            if (GLU) get(src + C / 2 * 4, un);
+            put_row(it, v, u);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = vn[i], u[i] = un[i];
+        }
+    };
+    auto all = [&](auto &&put_row) {
+        if constexpr (WK > 1) {
+#pragma unroll
+            for (int i = 0; i < MI; ++i) put_rows<PITCH>(acc, i, lds + (wk * MI + i) * 32 * PITCH);
+            __syncthreads();
+            if (r0 < ROWS) share([&](int it, float (&v)[8], float (&u)[8]) { put_row(wk * ROWS + it * RPI, v, u); }, wk * ROWS);
+        } else {
+#pragma unroll 1
+            for (int i = 0; i < MI; ++i) {
+                unrolled<MI>([&](auto I) {
+                    if (i == I.value) {
+                        put_rows<PITCH>(acc, I.value, lds);
+                        asm volatile("; rows %0" ::"i"(I.value) : "memory");   // the cases stay apart: registers have no index
+                    }
+                });
+                asm volatile("" ::: "memory");         // lanes read what others wrote: LDS keeps a wave's order
+                share([&](int it, float (&v)[8], float (&u)[8]) { put_row(i * 32 + it * RPI, v, u); }, 0);
+                asm volatile("" ::: "memory");
+            }
+        }
+    };
+    if (m0 >= p.M && WK == 1) return;
+    if constexpr (FIN == kFinPartial) {
+        const uint8_t *out = (const uint8_t *)(p.partials + (split * p.M + m0) * p.N);
+        const uint32_t row_b = (uint32_t)p.N * 4, bytes = (uint32_t)max(min(p.M - m0, (int64_t)kWideRows), (int64_t)0) * row_b;
+        const uint32_t vo = n < ncols ? r0 * row_b + (uint32_t)n * 4 : kOOB;
+        all([&](int row, float (&v)[8], float (&)[8]) {
+            buf_store(uintx4{f32_bits(v[0]), f32_bits(v[1]), f32_bits(v[2]), f32_bits(v[3])}, out, bytes, vo, row * row_b);
+            buf_store(uintx4{f32_bits(v[4]), f32_bits(v[5]), f32_bits(v[6]), f32_bits(v[7])}, out, bytes, vo, row * row_b + 16);
+        });
+    } else {
+        const FinishRows<FIN> fin(p.f, m0, p.M, r0, n, n < ncols);
+        Extra x = {}, more = {};
+        fin.fetch(x, WK > 1 ? wk * ROWS : 0);
+        all([&](int row, float (&v)[8], float (&u)[8]) {
+            fin.fetch(more, row + RPI);
+            fin.store(x, row, v, u);
+            x = more;
+        });
+    }
+}
+
+// OP: the operator, which says what there is to finish.
+template <int OP, int MI, int NJ, int WK, class Acc>
+__device__ __forceinline__ void finish_wave(const LinearParams &p, const Acc &acc, uint8_t *lds, int wk, int64_t m0,
+                                            int64_t n0, int64_t split)
+{
+    constexpr int PLAIN = OP == kLinDgrad ? kFinGrad : kFinFwd, GLU = OP == kLinDgrad ? kFinGradGlu : kFinFwdGlu;
+    if (p.f.finish == kFinPartial) finish_wave_as<kFinPartial, MI, NJ, WK>(p, acc, lds, wk, m0, n0, split);
+    else if (OP != kLinWgrad && p.f.finish == GLU) finish_wave_as<GLU, MI, NJ, WK>(p, acc, lds, wk, m0, n0, split);
+    else finish_wave_as<PLAIN, MI, NJ, WK>(p, acc, lds, wk, m0, n0, split);
+}
+
+// A workgroup's place in the product: its tile, its part of the reduction and the
+// operands' loads.
+template <bool ALA, bool ALB, int TM, int TN, int NT, int C>
+struct Place {
+    int64_t m0, n0, split;
+    int klen;
+    bool glu;
+    Operand<ALA, TM, NT, 0> a;
+    Operand<ALB, TN, NT, ALB ? C / 2 : 0> b;             // a wave has C columns
+
+    __device__ __forceinline__ void init(const LinearParams &p, int tilesM, int tilesN)
+    {
+        const uint32_t id = xcd_order(), tiles = (uint32_t)tilesM * (uint32_t)tilesN;
+        split = id / tiles;
+        int mt, nt;
+        grouped_tile_order((int)(id % tiles), tilesM, tilesN, mt, nt);
+        m0 = (int64_t)mt * TM;
+        glu = p.f.finish == kFinFwdGlu;
+        const int64_t kb = split * p.part;
+        klen = (int)min(p.K - kb, p.part);
+        // columns of the tile: n0 on; with SwiGLU, half as many gates and their ups, C / 2 of each to a wave
+        n0 = (int64_t)nt * (glu ? TN / 2 : TN);
+        const int64_t half = p.N >> 1;
+        const int rows = (int)min(p.M - m0, (int64_t)TM);
+        if (ALA) a.init(p.a + m0 * p.lda + kb, nullptr, rows, 0, 0, p.lda, klen, 0);
+        else a.init(p.a + kb * p.lda + m0, nullptr, 0, 0, 0, p.lda, klen, p.M - m0);
+        if (ALB) {
+            const int64_t n1 = glu ? half + n0 : n0 + C / 2;
+            const int rows0 = (int)min((glu ? half : p.N) - n0, (int64_t)(glu ? TN / 2 : TN));
+            b.init(p.b + n0 * p.ldb + kb, p.b + n1 * p.ldb + kb, rows0, glu ? rows0 : rows0 - C / 2, glu ? C / 2 : C, p.ldb, klen, 0);
+        } else {
+            b.init(p.b + kb * p.ldb + n0, nullptr, 0, 0, 0, p.ldb, klen, p.N - n0);
+        }
+    }
+    // first column of wave wn's outputs
+    __device__ __forceinline__ int64_t col(int wn) const { return n0 + wn * (glu ? C / 2 : C); }
+};
 
 template <bool ALA, bool ALB, int TM, int TN, int WM, int WN, int WK, int NS>
 __global__ __launch_bounds__(64 * WM * WN * WK, 2) void linear_kernel(LinearParams p, int tilesM, int tilesN)
@@ -392,34 +701,8 @@ __global__ __launch_bounds__(64 * WM * WN * WK, 2) void linear_kernel(LinearPara
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wk = wave % WK, wn = wave / WK % WN, wm = wave / WK / WN;
 
-    const uint32_t id = xcd_order(), tiles = (uint32_t)tilesM * (uint32_t)tilesN;
-    const int64_t split = id / tiles;
-    int mt, nt;
-    grouped_tile_order((int)(id % tiles), tilesM, tilesN, mt, nt);
-    const int64_t m0 = (int64_t)mt * TM;
-    const bool glu = p.f.finish == kFinFwdGlu;
-    const int64_t kb = split * p.part;
-    const int klen = (int)min(p.K - kb, p.part);
-    // columns of the tile: n0 on, or with SwiGLU TN / 2 gates from n0 and the
-    // same ups from N / 2 + n0
-    const int64_t n0 = (int64_t)nt * (glu ? TN / 2 : TN);
-    const int64_t half = p.N >> 1;
-
-    Operand<ALA, TM, NT> oa;
-    Operand<ALB, TN, NT> ob;
-    {
-        const int rows = (int)min(p.M - m0, (int64_t)TM);
-        if (ALA) oa.init(p.a + m0 * p.lda + kb, p.a + (m0 + TM / 2) * p.lda + kb, rows, rows - TM / 2, p.lda, klen, 0);
-        else oa.init(p.a + kb * p.lda + m0, nullptr, 0, 0, p.lda, klen, p.M - m0);
-        if (ALB) {
-            const int64_t n1 = glu ? half + n0 : n0 + TN / 2;
-            const int rows0 = (int)min((glu ? half : p.N) - n0, (int64_t)(glu ? TN / 2 : TN));
-            const int rows1 = glu ? rows0 : rows0 - TN / 2;
-            ob.init(p.b + n0 * p.ldb + kb, p.b + n1 * p.ldb + kb, rows0, rows1, p.ldb, klen, 0);
-        } else {
-            ob.init(p.b + kb * p.ldb + n0, nullptr, 0, 0, p.ldb, klen, p.N - n0);
-        }
-    }
+    Place<ALA, ALB, TM, TN, NT, NJ * 32> at;
+    at.init(p, tilesM, tilesN);
     const uint32_t lds0 = lds_addr(smem);
     Frags<ALA, TM, MI> ra;
     Frags<ALB, TN, NJ> rb;
@@ -441,15 +724,15 @@ __global__ __launch_bounds__(64 * WM * WN * WK, 2) void linear_kernel(LinearPara
                 acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bf[j], af[i], acc[i][j], 0, 0, 0);
     };
 
-    constexpr int LOADSN = Operand<ALA, TM, NT>::NL + Operand<ALB, TN, NT>::NL;
-    const int nk = (klen + kStage - 1) / kStage;
-    auto issue = [&](int kt, int slot) {
-        oa.issue(smem + slot * S::SLOT, kt * kStage, klen, wave);
-        ob.issue(smem + slot * S::SLOT + S::SLOTA, kt * kStage, klen, wave);
+    constexpr int LOADSN = decltype(at.a)::NL + decltype(at.b)::NL;
+    const int klen = at.klen, nk = (klen + kStage - 1) / kStage;
+    auto issue = [&](int slot) {
+        at.a.issue(smem + slot * S::SLOT, wave);
+        at.b.issue(smem + slot * S::SLOT + S::SLOTA, wave);
     };
     // stages past the end load zeros, so that the waits need no cases
 #pragma unroll
-    for (int st = 0; st < NS - 1; ++st) issue(st, st);
+    for (int st = 0; st < NS - 1; ++st) issue(st);
     if constexpr (WK == 1) {
         bf16x8 fa[2][MI], fb[2][NJ];
         wait_vmcnt<(NS - 2) * LOADSN>();
@@ -461,7 +744,7 @@ __global__ __launch_bounds__(64 * WM * WN * WK, 2) void linear_kernel(LinearPara
         for (int kt = 0; kt < nk; ++kt) {
             const uint32_t so = (uint32_t)slot * S::SLOT;
             const int freed = slot == 0 ? NS - 1 : slot - 1, next = slot + 1 == NS ? 0 : slot + 1;
-            issue(kt + NS - 1, freed);           // the slot that stage kt - 1 left at its closing barrier
+            issue(freed);           // the slot that stage kt - 1 left at its closing barrier
             ra.read(so, fa[1], IC<1>{});
             rb.read(so, fb[1], IC<1>{});
             mma(fa[0], fb[0]);
@@ -499,7 +782,7 @@ __global__ __launch_bounds__(64 * WM * WN * WK, 2) void linear_kernel(LinearPara
             default: ra.read(so, fa, IC<3>{}); rb.read(so, fb, IC<3>{}); break;
             }
             wait_frags(fa, fb);
-            issue(kt + NS - 1, slot == 0 ? NS - 1 : slot - 1);
+            issue(slot == 0 ? NS - 1 : slot - 1);
             mma(fa, fb);
             slot = slot + 1 == NS ? 0 : slot + 1;
         }
@@ -507,50 +790,133 @@ __global__ __launch_bounds__(64 * WM * WN * WK, 2) void linear_kernel(LinearPara
     wait_vmcnt<0>();                             // zeros of stages past the end may still be landing in the ring
     barrier();
 
-    // ---- the tile through LDS in fp32: lane l holds of block (i, j) row l % 32
-    // and columns (r / 4) 8 + (l / 32) 4 + r % 4
-    const int64_t ncols = glu ? half : p.N;
-#pragma unroll 1
-    for (int e0 = 0; e0 < TM; e0 += S::ER) {
-        const int row0 = wm * MI * 32 - e0;
-        if (e0) __syncthreads();
-#pragma unroll 1
-        for (int w = 0; w < WK; ++w) {
-            if (w) __syncthreads();
-            if (WK > 1 && w != wk) continue;
-            if (row0 < 0 || row0 >= S::ER) continue;
-#pragma unroll
-            for (int i = 0; i < MI; ++i)
-#pragma unroll
-                for (int j = 0; j < NJ; ++j)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        floatx4 *d = (floatx4 *)(smem + (row0 + i * 32 + (lane & 31)) * S::PITCH +
-                                                 (wn * NJ * 32 + j * 32 + q * 8 + (lane >> 5) * 4) * 4);
-                        floatx4 v = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-                        *d = w ? *d + v : v;
-                    }
-        }
-        __syncthreads();
-        const int groups = glu ? TN / 16 : TN / 8;
-        for (int i = threadIdx.x; i < S::ER * groups; i += NT) {
-            const int r = i / groups, g = i - r * groups;
-            const int64_t m = m0 + e0 + r, n = n0 + g * 8;
-            if (m >= p.M || n >= ncols) continue;
-            const uint8_t *src = smem + r * S::PITCH + g * 32;
-            float v[8], u[8];
-            *(floatx4 *)v = *(const floatx4 *)src;
-            *(floatx4 *)(v + 4) = *(const floatx4 *)(src + 16);
-            if (glu) {
-                *(floatx4 *)u = *(const floatx4 *)(src + TN / 2 * 4);
-                *(floatx4 *)(u + 4) = *(const floatx4 *)(src + TN / 2 * 4 + 16);
-            }
-            if (p.f.finish == kFinPartial) store_stream<true, false>(p.partials, (split * p.M + m) * p.N + n, v);
-            else finish8(p.f, m, n, v, u);
-        }
-    }
+    finish_wave<ALA ? ALB ? kLinFwd : kLinDgrad : kLinWgrad, MI, NJ, WK>(p, acc, smem + (WK > 1 ? 0 : wave * S::EPI), wk, at.m0 + wm * MI * 32, at.col(wn), at.split);
 }
 
+// ------------------------------------------------------------------ wide tile
+// The tile for products that fill the chip: 256 x 256 by four waves of 128 x 128,
+// one on each SIMD, with 256 accumulators each.  A wave's share is square because
+// LDS is the narrow place: for a step of 16 reduction values the waves read 4 x 8
+// KB here, eight waves of 128 x 64 6 KB each, which with the 16 KB that the loads
+// bring in would take LDS as long as the products take the matrix cores.
+//
+// One wave a SIMD hides nothing by itself, so the order of its instructions does:
+// a step's 16 products run while the next step's fragments are read and four loads
+// go out, each between two products (all 16 loads of a stage in one step held the
+// products up: 1259 TFLOP/s at 8192^3).  LDS holds three slots of A and two of B,
+// all of its 160 KB, so that the loads spread evenly over the four steps of stage t:
+//     B of t + 1, second half;  A of t + 2, first;  A of t + 2, second;  B of t + 2, first
+// The one barrier of a stage comes before its last step, whose operands are in
+// registers by then: it frees the stage's slots and hands out those of the next.
+constexpr int kWide = 256, kWideThreads = 256, kWideSlot = kWide * 128, kWideLds = 5 * kWideSlot;
+
+// Per-lane address in a stage of the wide tile of the fragment of a block of 16
+// rows / columns from `first`: lane l holds row / column l % 16 and reduction
+// values (l / 16) 8 on.
+template <bool ALONG>
+__device__ __forceinline__ uint32_t frag16_base(int first)
+{
+    const int lane = threadIdx.x & 63, r16 = lane & 15, q = lane >> 4;
+    if (ALONG) return (uint32_t)(first + r16) * 128 + (uint32_t)along(first + r16, q) * 16;
+    const int krow = q * 8 + (r16 >> 2), col = first + 4 * (r16 & 3);
+    return (uint32_t)krow * (kWide * 2) + (uint32_t)across<kWide / 8>(krow, col >> 3) * 16 + 8 * (r16 & 1);
+}
+
+// A wave's eight fragments of one operand at step KS (32 values) of a stage.
+template <bool ALONG>
+struct WideFrags {
+    uint32_t at;
+    __device__ __forceinline__ void init(uint32_t lds, int first) { at = lds + frag16_base<ALONG>(first); }
+    template <int KS, int I>
+    __device__ __forceinline__ bf16x8 read(uint32_t slot) const
+    {
+        if constexpr (ALONG) {
+            return __builtin_bit_cast(bf16x8, ldsr_u128<I * 16 * 128>((at + slot) ^ (uint32_t)(KS << 6)));     // chunk q + 4 KS
+        } else {
+            constexpr int O = KS * 32 * 512;
+            const uint32_t x = (at + slot) ^ (uint32_t)(I << 5);       // the rows' swizzle moves whole blocks
+            const uintx2 lo = read_tr<O>(x), hi = read_tr<O + 4 * 512>(x);
+            return __builtin_bit_cast(bf16x8, uintx4{lo[0], lo[1], hi[0], hi[1]});
+        }
+    }
+};
+
+template <bool ALA, bool ALB>
+__global__ __launch_bounds__(kWideThreads, 1) void linear_wide_kernel(LinearParams p, int tilesM, int tilesN)
+{
+    extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wn = wave & 1, wm = wave >> 1;
+    Place<ALA, ALB, kWide, kWide, kWideThreads, 128> at;
+    at.init(p, tilesM, tilesN);
+    const uint32_t lds0 = lds_addr(smem);
+    uint8_t *const smem_b = smem + 3 * kWideSlot;
+    WideFrags<ALA> ra;
+    WideFrags<ALB> rb;
+    ra.init(lds0, wm * 128);
+    rb.init(lds0 + 3 * kWideSlot, wn * 128);
+    floatx4 acc[8][8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[i][j] = floatx4{0, 0, 0, 0};
+    constexpr int NL = kWideSlot / 16 / kWideThreads;        // loads of an operand's stage
+    static_assert(NL == 8, "eight loads a step");
+    const int nk = (at.klen + kStage - 1) / kStage;
+    at.a.issue(smem, wave);
+    at.b.issue(smem_b, wave);
+    at.a.issue(smem + kWideSlot, wave);
+    at.b.issue(smem_b + kWideSlot, wave);
+    bf16x8 fa[2][8], fb[2][8];
+    wait_vmcnt<2 * NL>();
+    barrier();
+    unrolled<8>([&](auto I) { fa[0][I.value] = ra.template read<0, I.value>(0); });
+    unrolled<8>([&](auto I) { fb[0][I.value] = rb.template read<0, I.value>(0); });
+    wait_frags(fa[0], fb[0]);
+
+    uint32_t a0 = 0, a1 = kWideSlot, a2 = 2 * kWideSlot, b0 = 0, b1 = kWideSlot;     // slots of this stage and the next ones
+    auto step = [&](auto KC) {
+        constexpr int KS = decltype(KC)::value, C = KS, NKS = 1 - KS;
+        const uint32_t sa = KS ? a1 : a0, sb = KS ? b1 : b0;                         // where the next step's fragments are
+        const uint32_t v = KS ? at.b.lane_offset() : at.a.lane_offset();
+        unrolled<64>([&](auto X) {
+            constexpr int x = decltype(X)::value, i = x >> 3, j = x & 7;
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[C][j], fa[C][i], acc[i][j], 0, 0, 0);
+            if constexpr (x % 3 == 0 && x < 48) {
+                // in the order in which the next step needs them
+                constexpr int y = x / 3;
+                if constexpr (y == 0) fa[1 - C][0] = ra.template read<NKS, 0>(sa);
+                else if constexpr (y <= 8) fb[1 - C][y - 1] = rb.template read<NKS, y - 1>(sb);
+                else fa[1 - C][y - 8] = ra.template read<NKS, y - 8>(sa);
+            }
+            if constexpr (x % 8 == 4) {
+                if constexpr (KS == 0) at.a.issue_one(smem + a2, x / 8, v, wave);
+                else at.b.issue_one(smem_b + b0, x / 8, v, wave);
+            }
+            if constexpr (x % 2 == 1) __builtin_amdgcn_sched_barrier(0);
+        });
+        if constexpr (KS == 0) at.a.advance();
+        else at.b.advance();
+        wait_frags(fa[1 - C], fb[1 - C]);
+        if constexpr (KS == 0) {
+            wait_vmcnt<NL>();            // all but A of the stage after next has landed, for all waves after the barrier
+            barrier();
+        }
+    };
+    for (int kt = 0; kt < nk; ++kt) {
+        step(IC<0>{});
+        step(IC<1>{});
+        const uint32_t a = a0;
+        a0 = a1;
+        a1 = a2;
+        a2 = a;
+        b1 = b0;
+        b0 = kWideSlot - b1;
+    }
+    wait_vmcnt<0>();                     // zeros of stages past the end may still be landing in the ring
+    barrier();
+    finish_wave<ALA ? ALB ? kLinFwd : kLinDgrad : kLinWgrad, 4, 4, 1>(p, acc, smem + wave * 32 * wave_pitch<128>(), 0, at.m0 + wm * 128, at.col(wn), at.split);
+}
 
 // ------------------------------------------------------------------ few rows
 // At most 64 rows against w [N, K]: w is read once, x comes from L2.  A
@@ -644,44 +1010,45 @@ __global__ __launch_bounds__(kFewWaves * kWave) void linear_few_kernel(LinearPar
 #pragma unroll
     for (int i = 0; i < MT; ++i) *(floatx4 *)&red[wave][i * 16 + r16][q * 4] = acc[i];
     __syncthreads();
-    const int groups = glu ? 1 : 2;
-    for (int i = threadIdx.x; i < MT * 16 * groups; i += kFewWaves * kWave) {
-        const int m = i / groups, g = i % groups;
-        const int64_t nn = n0 + g * 8;
-        if (m >= p.M || (!glu && nn >= p.N)) continue;
-        float v[8] = {}, u[8] = {};
+    // a thread of the first waves finishes 8 columns of a row
+    const int groups = glu ? 1 : 2, m = threadIdx.x / groups, g = threadIdx.x % groups;
+    const int64_t nn = n0 + g * 8;
+    if (m >= p.M || (!glu && nn >= p.N)) return;
+    float v[8] = {}, u[8] = {};
 #pragma unroll
-        for (int wv = 0; wv < kFewWaves; ++wv)
+    for (int wv = 0; wv < kFewWaves; ++wv)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                v[j] += red[wv][m][g * 8 + j];
-                if (glu) u[j] += red[wv][m][8 + j];
-            }
-        finish8(p.f, m, nn, v, u);
-    }
+        for (int j = 0; j < 8; ++j) {
+            v[j] += red[wv][m][g * 8 + j];
+            if (glu) u[j] += red[wv][m][8 + j];
+        }
+    if (glu) finish_row<kFinFwdGlu>(p.f, m, nn, v, u);
+    else finish_row<kFinFwd>(p.f, m, nn, v, u);
 }
 
 // The parts' sums added in order, then what the tile itself would have done.
+template <int FIN>
 __global__ __launch_bounds__(kThreads) void linear_join_kernel(LinearParams p)
 {
-    const bool glu = p.f.finish == kFinFwdGlu;
-    const int64_t half = p.N >> 1, groups = (glu ? half : p.N) / 8, total = p.M * groups;
+    constexpr bool GLU = FIN == kFinFwdGlu;
+    const int64_t half = p.N >> 1, groups = (GLU ? half : p.N) / 8, total = p.M * groups;
     for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kThreads) {
         const int64_t m = i / groups, n = (i - m * groups) * 8;
         float v[8] = {}, u[8] = {};
+#pragma unroll 4
         for (int s = 0; s < p.splits; ++s) {
             float f[8];
             const int64_t at = (s * p.M + m) * p.N + n;
             load_stream<true, false>(p.partials, at, f);
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] += f[j];
-            if (glu) {
+            if (GLU) {
                 load_stream<true, false>(p.partials, at + half, f);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) u[j] += f[j];
             }
         }
-        finish8(p.f, m, n, v, u);
+        finish_row<FIN>(p.f, m, n, v, u);
     }
 }
 
@@ -698,7 +1065,12 @@ __global__ __launch_bounds__(kThreads) void colsum_kernel(const uint16_t *__rest
     float v[8] = {};
     if (n < N) {
 #pragma unroll 4
-        for (int64_t r = (int64_t)blockIdx.y * kColsumRows + side; r < M; r += (int64_t)gridDim.y * kColsumRows) add_row8(dy + r * N + n, v);
+        for (int64_t r = (int64_t)blockIdx.y * kColsumRows + side; r < M; r += (int64_t)gridDim.y * kColsumRows) {
+            float f[8];
+            unpack8(*(const uintx4 *)(dy + r * N + n), f);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] += f[j];
+        }
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) s[side][lane * 8 + j] = v[j];
@@ -723,6 +1095,7 @@ __global__ __launch_bounds__(kThreads) void colsum_join_kernel(const float *__re
     dbias[c] = accumulate ? dbias[c] + sum : sum;
 }
 
+template <int FIN>
 __global__ __launch_bounds__(kThreads) void act_bwd_kernel(const uint16_t *__restrict__ dout, FinishParams f, int64_t M)
 {
     const int64_t groups = f.N / 8, total = M * groups;
@@ -730,7 +1103,7 @@ __global__ __launch_bounds__(kThreads) void act_bwd_kernel(const uint16_t *__res
         const int64_t m = i / groups, n = (i - m * groups) * 8;
         float v[8], u[8];
         unpack8(*(const uintx4 *)(dout + m * f.N + n), v);
-        finish8(f, m, n, v, u);
+        finish_row<FIN>(f, m, n, v, u);
     }
 }
 
@@ -758,12 +1131,27 @@ hipError_t launch_tile(const LinearParams &p, hipStream_t s)
 }
 
 template <bool ALA, bool ALB>
+hipError_t launch_wide(const LinearParams &p, hipStream_t s)
+{
+    auto kern = linear_wide_kernel<ALA, ALB>;
+    static LdsLimit lds_limit;
+    const hipError_t e = lds_limit.ensure((const void *)kern, kWideLds);
+    if (e != hipSuccess) return e;
+    const bool glu = p.f.finish == kFinFwdGlu;
+    const int64_t cols = glu ? p.N / 2 : p.N, tn = glu ? kWide / 2 : kWide;
+    const int64_t tilesM = (p.M + kWide - 1) / kWide, tilesN = (cols + tn - 1) / tn;
+    hipLaunchKernelGGL(kern, dim3((unsigned)(tilesM * tilesN * p.splits)), dim3(kWideThreads), kWideLds, s, p, (int)tilesM,
+                       (int)tilesN);
+    return hipGetLastError();
+}
+
+template <bool ALA, bool ALB>
 hipError_t launch_op(const LinearParams &p, int tile, hipStream_t s)
 {
     switch (tile) {
-    case kTile256: return launch_tile<ALA, ALB, 256, 256, 2, 4, 1, 2>(p, s);
+    case kTile256: return launch_wide<ALA, ALB>(p, s);
     case kTile128: return launch_tile<ALA, ALB, 128, 128, 2, 2, 1, 2>(p, s);
-    default: return launch_tile<ALA, ALB, 64, 128, 1, 4, 1, 3>(p, s);
+    default: return launch_tile<ALA, ALB, 64, 128, 2, 2, 1, 3>(p, s);
     }
 }
 
@@ -821,7 +1209,13 @@ hipError_t launch_linear(const LinearParams &p0, int op, const LinearPlan &plan,
     p.f.finish = p0.f.finish;
     const int64_t items = p.M * ((p.f.finish == kFinFwdGlu ? p.N / 2 : p.N) / 8);
     const int64_t grid = (items + kThreads - 1) / kThreads;
-    hipLaunchKernelGGL(linear_join_kernel, dim3((unsigned)(grid > 16384 ? 16384 : grid)), dim3(kThreads), 0, s, p);
+    const dim3 g((unsigned)(grid > 16384 ? 16384 : grid)), b(kThreads);
+    switch (p.f.finish) {
+    case kFinFwd: hipLaunchKernelGGL(linear_join_kernel<kFinFwd>, g, b, 0, s, p); break;
+    case kFinFwdGlu: hipLaunchKernelGGL(linear_join_kernel<kFinFwdGlu>, g, b, 0, s, p); break;
+    case kFinGrad: hipLaunchKernelGGL(linear_join_kernel<kFinGrad>, g, b, 0, s, p); break;
+    default: hipLaunchKernelGGL(linear_join_kernel<kFinGradGlu>, g, b, 0, s, p); break;
+    }
     return hipGetLastError();
 }
 
@@ -858,7 +1252,9 @@ hipError_t launch_act_bwd(const uint16_t *dout, const uint16_t *c, uint16_t *dc,
     f.act = act;
     f.limit = limit;
     const int64_t grid = (M * (f.N / 8) + kThreads - 1) / kThreads;
-    hipLaunchKernelGGL(act_bwd_kernel, dim3((unsigned)(grid > 16384 ? 16384 : grid)), dim3(kThreads), 0, s, dout, f, M);
+    const dim3 g((unsigned)(grid > 16384 ? 16384 : grid)), b(kThreads);
+    if (act == kActSwiglu) hipLaunchKernelGGL(act_bwd_kernel<kFinGradGlu>, g, b, 0, s, dout, f, M);
+    else hipLaunchKernelGGL(act_bwd_kernel<kFinGrad>, g, b, 0, s, dout, f, M);
     return hipGetLastError();
 }
 
