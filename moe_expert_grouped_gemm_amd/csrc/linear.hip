@@ -174,7 +174,7 @@ struct Saved {
     uintx4 v, u;                          // kFinFwd*: the sums with bias, in bf16
 };
 
-template <int FIN>
+template <int FIN, bool F32>
 __device__ __forceinline__ Saved finish8(const FinishParams &p, const float (&bias)[8], const float (&bias_u)[8], const Extra &x,
                                          float (&v)[8], float (&u)[8])
 {
@@ -182,16 +182,15 @@ __device__ __forceinline__ Saved finish8(const FinishParams &p, const float (&bi
     if constexpr (FIN == kFinFwd || FIN == kFinFwdGlu) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] += bias[i];
-        if (FIN == kFinFwdGlu) {
+        saved.v = pack8(v);
+        if constexpr (FIN == kFinFwdGlu) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) u[i] += bias_u[i];
+            saved.u = pack8(u);
+            glu8(v, u, p.limit);
+        } else {
+            act8(v, p.act);
         }
-        if (p.save) {
-            saved.v = pack8(v);
-            if (FIN == kFinFwdGlu) saved.u = pack8(u);
-        }
-        if (FIN == kFinFwdGlu) glu8(v, u, p.limit);
-        else act8(v, p.act);
     } else if constexpr (FIN == kFinGrad) {
         float c[8];
         unpack8(x.c[0], c);
@@ -204,9 +203,9 @@ __device__ __forceinline__ Saved finish8(const FinishParams &p, const float (&bi
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = g[i], u[i] = w[i];
     }
-    if (FIN != kFinGradGlu && p.residual) {
+    if constexpr (FIN != kFinGradGlu) {                    // zeros where there is none
         float f[8];
-        if (p.f32) {
+        if constexpr (F32) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) f[i] = bits_f32(x.r[0][i]), f[4 + i] = bits_f32(x.r[1][i]);
         } else {
@@ -230,31 +229,33 @@ __device__ __forceinline__ void load_bias8(const FinishParams &p, int64_t n, flo
 }
 
 // One row, from its sums to memory.
-template <int FIN>
-__device__ __forceinline__ void finish_row(const FinishParams &p, int64_t m, int64_t n, float (&v)[8], float (&u)[8])
+template <int FIN, bool F32>
+__device__ __forceinline__ void finish_row_as(const FinishParams &p, int64_t m, int64_t n, float (&v)[8], float (&u)[8])
 {
     const int64_t at = m * p.ldo + n;
     float bias[8], bias_u[8];
     load_bias8<FIN>(p, n, bias, bias_u);
     Extra x = {};
     if (FIN != kFinGradGlu && p.residual) {
-        if (p.f32) {
-            x.r[0] = *(const uintx4 *)((const float *)p.residual + at);
-            x.r[1] = *(const uintx4 *)((const float *)p.residual + at + 4);
-        } else {
-            x.r[0] = *(const uintx4 *)((const uint16_t *)p.residual + at);
-        }
+        x.r[0] = *(const uintx4 *)((const uint8_t *)p.residual + at * (F32 ? 4 : 2));
+        if (F32) x.r[1] = *(const uintx4 *)((const uint8_t *)p.residual + at * 4 + 16);
     }
     if ((FIN == kFinGrad && p.c) || FIN == kFinGradGlu) x.c[0] = *(const uintx4 *)(p.c + at);
     if (FIN == kFinGradGlu) x.c[1] = *(const uintx4 *)(p.c + at + p.N);
-    const Saved s = finish8<FIN>(p, bias, bias_u, x, v, u);
+    const Saved s = finish8<FIN, F32>(p, bias, bias_u, x, v, u);
     if ((FIN == kFinFwd || FIN == kFinFwdGlu) && p.save) {
         *(uintx4 *)(p.save + m * p.N + n) = s.v;
         if (FIN == kFinFwdGlu) *(uintx4 *)(p.save + m * p.N + (p.N >> 1) + n) = s.u;
     }
-    if (p.f32) store_stream<true, false>(p.out, at, v);
-    else store_stream<false, false>(p.out, at, v);
+    store_stream<F32, false>(p.out, at, v);
     if (FIN == kFinGradGlu) store_stream<false, false>(p.out, at + p.N, u);
+}
+
+template <int FIN>
+__device__ __forceinline__ void finish_row(const FinishParams &p, int64_t m, int64_t n, float (&v)[8], float (&u)[8])
+{
+    if (FIN < kFinGrad && p.f32) finish_row_as<FIN, true>(p, m, n, v, u);
+    else finish_row_as<FIN, false>(p, m, n, v, u);
 }
 
 // 16 bytes of a buffer at `base`; at or past `bytes` zeros are read and nothing is
@@ -273,7 +274,7 @@ __device__ __forceinline__ void buf_store(uintx4 v, const void *base, uint32_t b
 // have no branch around them -- what is not there has a bound of 0 -- so that the
 // wait for a row's loads is a count that leaves the stores in flight (with a
 // branch it was for every store before: 1000 cycles a row).
-template <int FIN>
+template <int FIN, bool F32>
 struct FinishRows {
     static constexpr bool FWD = FIN == kFinFwd || FIN == kFinFwdGlu;
     const FinishParams &p;
@@ -282,14 +283,13 @@ struct FinishRows {
     uint32_t vo, vs;                      // this lane's offsets in out (and residual and c) and in save
     uint32_t ldo_b, lds_b;                // bytes of a row
     uint32_t far_o, far_s;                // from the gates' columns to the ups'
-    uint32_t hi;                          // from the first 16 bytes of 8 outputs to the second, or out of bounds
     float bias[8], bias_u[8];
 
     __device__ __forceinline__ FinishRows(const FinishParams &f, int64_t m0, int64_t M, int r0, int64_t n, bool live) : p(f)
     {
         const int rows = (int)min(M - m0, (int64_t)kWideRows);
-        const uint32_t size = f.f32 ? 4 : 2;
-        ldo_b = (uint32_t)f.ldo * size;
+        constexpr uint32_t SIZE = F32 ? 4 : 2;
+        ldo_b = (uint32_t)f.ldo * SIZE;
         lds_b = (uint32_t)f.N * 2;
         out = (const uint8_t *)f.out + m0 * ldo_b;
         out_b = rows > 0 ? rows * ldo_b : 0;
@@ -299,35 +299,33 @@ struct FinishRows {
         sv_b = f.save && rows > 0 ? rows * lds_b : 0;
         cs = (const uint8_t *)f.c + m0 * ldo_b;
         cs_b = f.c ? out_b : 0;
-        vo = live ? r0 * ldo_b + (uint32_t)n * size : kOOB;
+        vo = live ? r0 * ldo_b + (uint32_t)n * SIZE : kOOB;
         vs = live ? r0 * lds_b + (uint32_t)n * 2 : kOOB;
         far_o = (uint32_t)f.N * 2;
         far_s = (uint32_t)f.N;            // N / 2 columns
-        hi = f.f32 ? 16 : kOOB;
         load_bias8<FIN>(f, live ? n : 0, bias, bias_u);
     }
     // `row` rows after this lane's first
     __device__ __forceinline__ void fetch(Extra &x, uint32_t row) const
     {
         const uint32_t s = row * ldo_b;
-        if (FIN != kFinGradGlu) {
-            x.r[0] = buf_load(res, res_b, vo, s);
-            x.r[1] = buf_load(res, res_b, vo | (hi & kOOB), s + (hi & 16));
-        }
+        if (FIN != kFinGradGlu) x.r[0] = buf_load(res, res_b, vo, s);
+        if (F32) x.r[1] = buf_load(res, res_b, vo, s + 16);
         if (!FWD) x.c[0] = buf_load(cs, cs_b, vo, s);
         if (FIN == kFinGradGlu) x.c[1] = buf_load(cs, cs_b, vo, s + far_o);
     }
     __device__ __forceinline__ void store(const Extra &x, uint32_t row, float (&v)[8], float (&u)[8]) const
     {
-        const Saved sv8 = finish8<FIN>(p, bias, bias_u, x, v, u);
+        const Saved sv8 = finish8<FIN, F32>(p, bias, bias_u, x, v, u);
         const uint32_t s = row * ldo_b;
         if (FWD) buf_store(sv8.v, sv, sv_b, vs, row * lds_b);
         if (FIN == kFinFwdGlu) buf_store(sv8.u, sv, sv_b, vs, row * lds_b + far_s);
-        uintx4 a, b = {f32_bits(v[4]), f32_bits(v[5]), f32_bits(v[6]), f32_bits(v[7])};
-        if (p.f32) a = uintx4{f32_bits(v[0]), f32_bits(v[1]), f32_bits(v[2]), f32_bits(v[3])};
-        else a = pack8(v);
-        buf_store(a, out, out_b, vo, s);
-        if (FWD) buf_store(b, out, out_b, vo | (hi & kOOB), s + (hi & 16));
+        if constexpr (F32) {
+            buf_store(uintx4{f32_bits(v[0]), f32_bits(v[1]), f32_bits(v[2]), f32_bits(v[3])}, out, out_b, vo, s);
+            buf_store(uintx4{f32_bits(v[4]), f32_bits(v[5]), f32_bits(v[6]), f32_bits(v[7])}, out, out_b, vo, s + 16);
+        } else {
+            buf_store(pack8(v), out, out_b, vo, s);
+        }
         if (FIN == kFinGradGlu) buf_store(pack8(u), out, out_b, vo, s + far_o);
     }
 };
@@ -341,7 +339,7 @@ __device__ __forceinline__ int along(int r, int c) { return c ^ ((r >> 1) & 7); 
 template <int CPR>
 __device__ __forceinline__ int across(int k, int c)
 {
-    return CPR >= 16 ? c ^ ((k & 3) << 2) : c ^ (((k >> 1) & 1) << 2);
+    return CPR >= 32 ? c ^ ((k & 3) << 2) ^ (((k >> 3) & 1) << 1) : CPR == 16 ? c ^ ((k & 3) << 2) : c ^ (((k >> 1) & 1) << 2);
 }
 
 // One operand of a tile: R rows (ALONG) or columns (!ALONG) of a stage, loaded
@@ -365,6 +363,7 @@ struct Operand {
     int k;                                                 // ALONG: this lane's first reduction value
     int klen, k0;                                          // reduction values, and those before the stage
     uint32_t pitch, width;                                 // !ALONG: bytes of a row, and of its valid columns
+    uint32_t odd;                                          // !ALONG, long rows: voff of the odd loads, whose swizzle differs
 
     // rows0, rows1: valid rows from p0 and p1 (ALONG); pair: rows of base[0] from pair to pair; cols: valid columns (!ALONG)
     __device__ __forceinline__ void init(const uint16_t *p0, const uint16_t *p1, int rows0, int rows1, int pair, int64_t ld,
@@ -400,6 +399,8 @@ struct Operand {
             pitch = (uint32_t)ld * 2;
             width = (uint32_t)min(cols, (int64_t)R) * 2;
             voff = row * pitch + (uint32_t)min((int64_t)chunk * 8, cols - 8) * 2;
+            static_assert(CPR < 32 || RPL == 8, "a load is one octet of rows");
+            odd = CPR < 32 ? voff : row * pitch + (uint32_t)min((int64_t)across<CPR>(row + 8, t % CPR) * 8, cols - 8) * 2;
             step = kStage * ld * 2;
             k = 0;
             bound();
@@ -419,6 +420,7 @@ struct Operand {
     {
         constexpr int LPG = HALVES == 2 ? PAIR / RPL : NL;           // loads of a group
         const int q = i / LPG, h = HALVES == 2 ? q & 1 : 0;
+        if (!ALONG && CPR >= 32 && (i & 1)) v = odd;
         dma16(base[h], bytes[h], lds + wave * kWave * 16 + i * NT * 16, v, (HALVES == 2 ? (q >> 1) * pstep : 0u) + (i % LPG) * rstep);
     }
     __device__ __forceinline__ void advance()
@@ -563,7 +565,7 @@ __device__ __forceinline__ void put_rows(const floatx4 (&acc)[MI][NJ], int i, ui
             *(floatx4 *)(to + (h * 16 + (lane & 15)) * PITCH + (j * 16 + (lane >> 4) * 4) * 4) = acc[2 * i + h][j];
 }
 
-template <int FIN, int MI, int NJ, int WK, class Acc>
+template <int FIN, bool F32, int MI, int NJ, int WK, class Acc>
 __device__ __forceinline__ void finish_wave_as(const LinearParams &p, const Acc &acc, uint8_t *lds, int wk, int64_t m0,
                                                int64_t n0, int64_t split)
 {
@@ -584,21 +586,28 @@ __device__ __forceinline__ void finish_wave_as(const LinearParams &p, const Acc 
             }
         }
     };
-    // rows of LDS from `from` on; the next row's loads go out before one is worked on.  Loops, not copies: a wide tile's
-    // all unrolled were 350 KB of code that each workgroup had to fetch
+    // rows of LDS from `from` on; the next row's loads go out before one is worked on, in pairs that take each other's
+    // registers.  Loops, not copies: a wide tile's all unrolled were 350 KB of code that each workgroup had to fetch
     auto share = [&](auto &&put_row, int from) {
         const uint8_t *src = lds + (from + r0) * PITCH + g * 32;
-        float v[8], u[8], vn[8], un[8];
-        get(src, v);
-        if (GLU) get(src + C / 2 * 4, u);
+        float v0[8], u0[8], v1[8], u1[8];
+        auto next = [&](int it, float (&v)[8], float (&u)[8]) {
+            const uint8_t *s = src + min(it, ITS - 1) * RPI * PITCH;
+            get(s, v);
+            if (GLU) get(s + C / 2 * 4, u);
+        };
+        next(0, v0, u0);
+        if constexpr (ITS == 1) {
+            put_row(IC<0>{}, 0, v0, u0);
+        } else {
+            static_assert(ITS % 2 == 0, "rows in pairs");
 #pragma unroll 1
-        for (int it = 0; it < ITS; ++it) {
-            if (it + 1 < ITS) src += RPI * PITCH;
-            get(src, vn);
-            if (GLU) get(src + C / 2 * 4, un);
-            put_row(it, v, u);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = vn[i], u[i] = un[i];
+            for (int it = 0; it < ITS; it += 2) {
+                next(it + 1, v1, u1);
+                put_row(IC<0>{}, it, v0, u0);
+                next(it + 2, v0, u0);
+                put_row(IC<1>{}, it + 1, v1, u1);
+            }
         }
     };
     auto all = [&](auto &&put_row) {
@@ -606,7 +615,7 @@ __device__ __forceinline__ void finish_wave_as(const LinearParams &p, const Acc 
 #pragma unroll
             for (int i = 0; i < MI; ++i) put_rows<PITCH>(acc, i, lds + (wk * MI + i) * 32 * PITCH);
             __syncthreads();
-            if (r0 < ROWS) share([&](int it, float (&v)[8], float (&u)[8]) { put_row(wk * ROWS + it * RPI, v, u); }, wk * ROWS);
+            if (r0 < ROWS) share([&](auto P, int it, float (&v)[8], float (&u)[8]) { put_row(P, wk * ROWS + it * RPI, v, u); }, wk * ROWS);
         } else {
 #pragma unroll 1
             for (int i = 0; i < MI; ++i) {
@@ -617,7 +626,7 @@ __device__ __forceinline__ void finish_wave_as(const LinearParams &p, const Acc 
                     }
                 });
                 asm volatile("" ::: "memory");         // lanes read what others wrote: LDS keeps a wave's order
-                share([&](int it, float (&v)[8], float (&u)[8]) { put_row(i * 32 + it * RPI, v, u); }, 0);
+                share([&](auto P, int it, float (&v)[8], float (&u)[8]) { put_row(P, i * 32 + it * RPI, v, u); }, 0);
                 asm volatile("" ::: "memory");
             }
         }
@@ -627,18 +636,18 @@ __device__ __forceinline__ void finish_wave_as(const LinearParams &p, const Acc 
         const uint8_t *out = (const uint8_t *)(p.partials + (split * p.M + m0) * p.N);
         const uint32_t row_b = (uint32_t)p.N * 4, bytes = (uint32_t)max(min(p.M - m0, (int64_t)kWideRows), (int64_t)0) * row_b;
         const uint32_t vo = n < ncols ? r0 * row_b + (uint32_t)n * 4 : kOOB;
-        all([&](int row, float (&v)[8], float (&)[8]) {
+        all([&](auto, int row, float (&v)[8], float (&)[8]) {
             buf_store(uintx4{f32_bits(v[0]), f32_bits(v[1]), f32_bits(v[2]), f32_bits(v[3])}, out, bytes, vo, row * row_b);
             buf_store(uintx4{f32_bits(v[4]), f32_bits(v[5]), f32_bits(v[6]), f32_bits(v[7])}, out, bytes, vo, row * row_b + 16);
         });
     } else {
-        const FinishRows<FIN> fin(p.f, m0, p.M, r0, n, n < ncols);
-        Extra x = {}, more = {};
-        fin.fetch(x, WK > 1 ? wk * ROWS : 0);
-        all([&](int row, float (&v)[8], float (&u)[8]) {
-            fin.fetch(more, row + RPI);
-            fin.store(x, row, v, u);
-            x = more;
+        const FinishRows<FIN, F32> fin(p.f, m0, p.M, r0, n, n < ncols);
+        Extra x[2] = {};
+        fin.fetch(x[0], WK > 1 ? wk * ROWS : 0);
+        all([&](auto P, int row, float (&v)[8], float (&u)[8]) {
+            constexpr int I = decltype(P)::value;
+            if (ITS > 1) fin.fetch(x[1 - I], row + RPI);
+            fin.store(x[I], row, v, u);
         });
     }
 }
@@ -649,9 +658,19 @@ __device__ __forceinline__ void finish_wave(const LinearParams &p, const Acc &ac
                                             int64_t n0, int64_t split)
 {
     constexpr int PLAIN = OP == kLinDgrad ? kFinGrad : kFinFwd, GLU = OP == kLinDgrad ? kFinGradGlu : kFinFwdGlu;
-    if (p.f.finish == kFinPartial) finish_wave_as<kFinPartial, MI, NJ, WK>(p, acc, lds, wk, m0, n0, split);
-    else if (OP != kLinWgrad && p.f.finish == GLU) finish_wave_as<GLU, MI, NJ, WK>(p, acc, lds, wk, m0, n0, split);
-    else finish_wave_as<PLAIN, MI, NJ, WK>(p, acc, lds, wk, m0, n0, split);
+    auto as = [&](auto F, auto F32) {
+        finish_wave_as<decltype(F)::value, decltype(F32)::value, MI, NJ, WK>(p, acc, lds, wk, m0, n0, split);
+    };
+    if (p.f.finish == kFinPartial) {
+        as(IC<kFinPartial>{}, IC<true>{});
+    } else if (OP != kLinWgrad && p.f.finish == GLU) {
+        if (OP == kLinFwd && p.f.f32) as(IC<GLU>{}, IC<OP == kLinFwd>{});
+        else as(IC<GLU>{}, IC<false>{});
+    } else if (OP == kLinWgrad || (OP == kLinFwd && p.f.f32)) {
+        as(IC<PLAIN>{}, IC<OP != kLinDgrad>{});
+    } else {
+        as(IC<PLAIN>{}, IC<OP == kLinWgrad>{});
+    }
 }
 
 // A workgroup's place in the product: its tile, its part of the reduction and the
