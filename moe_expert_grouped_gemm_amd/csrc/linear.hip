@@ -447,8 +447,8 @@ __device__ __forceinline__ uintx2 read_tr(uint32_t addr)
     return v;
 }
 
-// Fragments of NB blocks of 32 rows / columns at reduction step KS (16 values)
-// of a stage.  at: per-lane address in the stage (frag_base), plus the slot.
+// Per-lane address in a stage of the fragment of a block of 32 rows / columns from
+// `first`: lane l holds row / column l % 32 and reduction values (l / 32) 8 on.
 template <bool ALONG, int R>
 __device__ __forceinline__ uint32_t frag_base(int first)
 {
@@ -461,32 +461,20 @@ __device__ __forceinline__ uint32_t frag_base(int first)
     return (uint32_t)krow * (R * 2) + (uint32_t)across<R / 8>(krow, col >> 3) * 16 + 8 * (s16 & 1);
 }
 
-template <bool ALONG, int R, int NB>
+template <bool ALONG, int R>
 struct Frags {
     uint32_t at;
     __device__ __forceinline__ void init(uint32_t lds, int first) { at = lds + frag_base<ALONG, R>(first); }
-    template <int KS>
-    __device__ __forceinline__ void read(uint32_t slot, bf16x8 (&f)[NB], IC<KS>) const
+    template <int KS, int I>
+    __device__ __forceinline__ bf16x8 read(uint32_t slot) const
     {
         if constexpr (ALONG) {
-            read_along<0>((at + slot) ^ (uint32_t)(KS << 5), f);
+            return __builtin_bit_cast(bf16x8, ldsr_u128<I * 32 * 128>((at + slot) ^ (uint32_t)(KS << 5)));
         } else {
             constexpr int O = KS * 16 * R * 2;
-#pragma unroll
-            for (int i = 0; i < NB; ++i) {
-                // a block's 64 bytes: the rows' swizzle moves whole ones
-                const uint32_t a = (at + slot) ^ (uint32_t)(i << 6);
-                const uintx2 lo = read_tr<O>(a), hi = read_tr<O + 4 * R * 2>(a);
-                f[i] = __builtin_bit_cast(bf16x8, uintx4{lo[0], lo[1], hi[0], hi[1]});
-            }
-        }
-    }
-    template <int I>
-    __device__ __forceinline__ void read_along(uint32_t a, bf16x8 (&f)[NB]) const
-    {
-        if constexpr (I < NB) {
-            f[I] = __builtin_bit_cast(bf16x8, ldsr_u128<I * 32 * 128>(a));
-            read_along<I + 1>(a, f);
+            const uint32_t a = (at + slot) ^ (uint32_t)(I << 6);       // a block's 64 bytes: the rows' swizzle moves whole ones
+            const uintx2 lo = read_tr<O>(a), hi = read_tr<O + 4 * R * 2>(a);
+            return __builtin_bit_cast(bf16x8, uintx4{lo[0], lo[1], hi[0], hi[1]});
         }
     }
 };
@@ -502,15 +490,6 @@ __device__ __forceinline__ void wait_frags(bf16x8 (&a)[NA], bf16x8 (&b)[NB])
 #pragma unroll
     for (int i = 0; i < NB; ++i) asm volatile("" : "+v"(b[i]));
 }
-template <int NA, int NB>
-__device__ __forceinline__ void pin_frags(bf16x8 (&a)[NA], bf16x8 (&b)[NB])
-{
-#pragma unroll
-    for (int i = 0; i < NA; ++i) asm volatile("" : "+v"(a[i]));
-#pragma unroll
-    for (int i = 0; i < NB; ++i) asm volatile("" : "+v"(b[i]));
-}
-
 // ------------------------------------------------------------------ kernel
 // Bytes of a row of C fp32 sums in LDS: 16 more, so that rows start on other banks.
 template <int C>
@@ -723,10 +702,12 @@ __global__ __launch_bounds__(64 * WM * WN * WK, 2) void linear_kernel(LinearPara
     Place<ALA, ALB, TM, TN, NT, NJ * 32> at;
     at.init(p, tilesM, tilesN);
     const uint32_t lds0 = lds_addr(smem);
-    Frags<ALA, TM, MI> ra;
-    Frags<ALB, TN, NJ> rb;
+    Frags<ALA, TM> ra;
+    Frags<ALB, TN> rb;
     ra.init(lds0, wm * MI * 32);
     rb.init(lds0 + S::SLOTA, wn * NJ * 32);
+    static_assert(WK == 1 || (ALA && ALB), "waves that share a stage's steps read along the reduction");
+    if (WK > 1) ra.at ^= (uint32_t)wk << 5, rb.at ^= (uint32_t)wk << 5;      // the wave's own step
 
     floatx16 acc[MI][NJ];
 #pragma unroll
@@ -735,74 +716,79 @@ __global__ __launch_bounds__(64 * WM * WN * WK, 2) void linear_kernel(LinearPara
         for (int j = 0; j < NJ; ++j)
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
-    auto mma = [&](const bf16x8 (&af)[MI], const bf16x8 (&bf)[NJ]) {
-#pragma unroll
-        for (int i = 0; i < MI; ++i)
-#pragma unroll
-            for (int j = 0; j < NJ; ++j)
-                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bf[j], af[i], acc[i][j], 0, 0, 0);
-    };
-
-    constexpr int LOADSN = decltype(at.a)::NL + decltype(at.b)::NL;
-    const int klen = at.klen, nk = (klen + kStage - 1) / kStage;
+    constexpr int LA = decltype(at.a)::NL, L = LA + decltype(at.b)::NL;       // loads of a stage
+    const int nk = (at.klen + kStage - 1) / kStage;
     auto issue = [&](int slot) {
         at.a.issue(smem + slot * S::SLOT, wave);
         at.b.issue(smem + slot * S::SLOT + S::SLOTA, wave);
     };
     // stages past the end load zeros, so that the waits need no cases
-#pragma unroll
-    for (int st = 0; st < NS - 1; ++st) issue(st);
     if constexpr (WK == 1) {
-        bf16x8 fa[2][MI], fb[2][NJ];
-        wait_vmcnt<(NS - 2) * LOADSN>();
+        // A stage's fragments are read while the one before is multiplied, so that LDS's latency is paid once a stage and
+        // the slot is free again as soon as all waves hold them: NS stages are under way beside the one in registers
+        bf16x8 fa[2][4][MI], fb[2][4][NJ];
+        constexpr int P = 4 * MI * NJ, R = 4 * (MI + NJ);    // products and reads of a stage
+#pragma unroll
+        for (int st = 0; st < NS; ++st) issue(st);
+        wait_vmcnt<(NS - 1) * L>();
         barrier();
-        ra.read(0, fa[0], IC<0>{});
-        rb.read(0, fb[0], IC<0>{});
-        wait_frags(fa[0], fb[0]);
-        int slot = 0;
-        for (int kt = 0; kt < nk; ++kt) {
-            const uint32_t so = (uint32_t)slot * S::SLOT;
-            const int freed = slot == 0 ? NS - 1 : slot - 1, next = slot + 1 == NS ? 0 : slot + 1;
-            issue(freed);           // the slot that stage kt - 1 left at its closing barrier
-            ra.read(so, fa[1], IC<1>{});
-            rb.read(so, fb[1], IC<1>{});
-            mma(fa[0], fb[0]);
-            wait_frags(fa[1], fb[1]);
-            ra.read(so, fa[0], IC<2>{});
-            rb.read(so, fb[0], IC<2>{});
-            mma(fa[1], fb[1]);
-            wait_frags(fa[0], fb[0]);
-            ra.read(so, fa[1], IC<3>{});
-            rb.read(so, fb[1], IC<3>{});
-            mma(fa[0], fb[0]);
-            wait_frags(fa[1], fb[1]);
-            wait_vmcnt<(NS - 2) * LOADSN>();     // stage kt + 1 has landed for this wave, and after the barrier for all
+        unrolled<4>([&](auto KS) {
+            unrolled<MI>([&](auto I) { fa[0][KS.value][I.value] = ra.template read<KS.value, I.value>(0); });
+            unrolled<NJ>([&](auto I) { fb[0][KS.value][I.value] = rb.template read<KS.value, I.value>(0); });
+        });
+        unrolled<4>([&](auto KS) { wait_frags(fa[0][KS.value], fb[0][KS.value]); });
+        uint32_t slot = 0, next = NS == 1 ? 0 : S::SLOT;
+        auto stage = [&](auto CC) {
+            constexpr int C = decltype(CC)::value;
+            wait_vmcnt<(NS - 2) * L>();              // the next stage has landed for this wave, and after the barrier for all
             barrier();
-            const uint32_t sn = (uint32_t)next * S::SLOT;
-            ra.read(sn, fa[0], IC<0>{});
-            rb.read(sn, fb[0], IC<0>{});
-            pin_frags(fa[1], fb[1]);
-            mma(fa[1], fb[1]);
-            wait_frags(fa[0], fb[0]);
+            const uint32_t va = at.a.lane_offset(), vb = at.b.lane_offset();
+            unrolled<P>([&](auto X) {
+                constexpr int x = decltype(X)::value, ks = x / (MI * NJ), i = x / NJ % MI, j = x % NJ;
+                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[C][ks][j], fa[C][ks][i], acc[i][j], 0, 0, 0);
+                unrolled<(x + 1) * R / P - x * R / P>([&](auto Y) {
+                    constexpr int y = x * R / P + decltype(Y)::value, k = y / (MI + NJ), q = y % (MI + NJ);
+                    if constexpr (q < MI) fa[1 - C][k][q] = ra.template read<k, q>(next);
+                    else fb[1 - C][k][q - MI] = rb.template read<k, q - MI>(next);
+                });
+                unrolled<(x + 1) * L / P - x * L / P>([&](auto Y) {
+                    constexpr int y = x * L / P + decltype(Y)::value;
+                    if constexpr (y < LA) at.a.issue_one(smem + slot, y, va, wave);
+                    else at.b.issue_one(smem + slot + S::SLOTA, y - LA, vb, wave);
+                });
+                __builtin_amdgcn_sched_barrier(0);
+            });
+            at.a.advance();
+            at.b.advance();
+            unrolled<4>([&](auto KS) { wait_frags(fa[1 - C][KS.value], fb[1 - C][KS.value]); });
             slot = next;
+            next = next == (NS - 1) * S::SLOT ? 0 : next + S::SLOT;
+        };
+        int kt = 0;
+        for (; kt + 2 <= nk; kt += 2) {
+            stage(IC<0>{});
+            stage(IC<1>{});
         }
+        if (kt < nk) stage(IC<0>{});
     } else {
         static_assert(WK == 4, "a step of the stage per wave");
+#pragma unroll
+        for (int st = 0; st < NS - 1; ++st) issue(st);
         bf16x8 fa[MI], fb[NJ];
         int slot = 0;
         for (int kt = 0; kt < nk; ++kt) {
-            wait_vmcnt<(NS - 2) * LOADSN>();
+            wait_vmcnt<(NS - 2) * L>();
             barrier();
             const uint32_t so = (uint32_t)slot * S::SLOT;
-            switch (wk) {
-            case 0: ra.read(so, fa, IC<0>{}); rb.read(so, fb, IC<0>{}); break;
-            case 1: ra.read(so, fa, IC<1>{}); rb.read(so, fb, IC<1>{}); break;
-            case 2: ra.read(so, fa, IC<2>{}); rb.read(so, fb, IC<2>{}); break;
-            default: ra.read(so, fa, IC<3>{}); rb.read(so, fb, IC<3>{}); break;
-            }
+            unrolled<MI>([&](auto I) { fa[I.value] = ra.template read<0, I.value>(so); });
+            unrolled<NJ>([&](auto I) { fb[I.value] = rb.template read<0, I.value>(so); });
             wait_frags(fa, fb);
             issue(slot == 0 ? NS - 1 : slot - 1);
-            mma(fa, fb);
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
+#pragma unroll
+                for (int j = 0; j < NJ; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[j], fa[i], acc[i][j], 0, 0, 0);
             slot = slot + 1 == NS ? 0 : slot + 1;
         }
     }
@@ -938,7 +924,7 @@ __global__ __launch_bounds__(kWideThreads, 1) void linear_wide_kernel(LinearPara
 }
 
 // ------------------------------------------------------------------ few rows
-// At most 64 rows against w [N, K]: w is read once, x comes from L2.  A
+// At most 16 rows against w [N, K]: w is read once, x comes from L2.  A
 // workgroup takes 16 columns (8 gates and their ups), its eight waves the
 // steps of 64 reduction values in turn: a wave's loads of a step are whole
 // lines of 16 rows.  The reduction's values are taken in the order in which a
@@ -946,10 +932,9 @@ __global__ __launch_bounds__(kWideThreads, 1) void linear_wide_kernel(LinearPara
 // sums meet in LDS and are added in order.
 constexpr int kFewWaves = 8, kFewCols = 16;
 
-template <int MT>
 __global__ __launch_bounds__(kFewWaves * kWave) void linear_few_kernel(LinearParams p)
 {
-    constexpr int U = MT == 1 ? 4 : 2;                       // steps of a batch; two batches are in flight
+    constexpr int MT = 1, U = 4;                             // steps of a batch; two batches are in flight
     constexpr int PITCH = kFewCols + 4;
     __shared__ __attribute__((aligned(16))) float red[kFewWaves][MT * 16][PITCH];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -1054,7 +1039,7 @@ __global__ __launch_bounds__(kThreads) void linear_join_kernel(LinearParams p)
     for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kThreads) {
         const int64_t m = i / groups, n = (i - m * groups) * 8;
         float v[8] = {}, u[8] = {};
-#pragma unroll 4
+#pragma unroll 8
         for (int s = 0; s < p.splits; ++s) {
             float f[8];
             const int64_t at = (s * p.M + m) * p.N + n;
@@ -1127,12 +1112,29 @@ __global__ __launch_bounds__(kThreads) void act_bwd_kernel(const uint16_t *__res
 }
 
 // ------------------------------------------------------------------ plan and launch
-enum Tile { kTileFew = 0, kTile256 = 1, kTile128 = 2, kTile64 = 3, kTileNarrow = 4 };
-struct TileShape {
-    int tm, tn, per_cu;      // workgroups of it that a CU holds
-    float stage;             // us of a stage while a CU holds them
+// The tiles, with what a call of theirs costs in us: `fixed` (launch, first loads,
+// epilogue) and a stage of 64 reduction values while a CU holds one workgroup and,
+// where two fit, while it holds two.  Measured on forward products of 1021 x 2880 x
+// 2880, 45 to 4096 x 4096 x 4096 and slices of their reduction; the other layouts
+// take up to a fifth longer, alike for all tiles.  The deep ones keep a CU's LDS for
+// one workgroup's ring, which pays where there are too few tiles for two.
+enum Tile {
+    kTileFew = 0, kTile256 = 1, kTile128 = 2, kTile64 = 3, kTileNarrow = 4, kTile128Deep = 5, kTile64Deep = 6, kTile32Deep = 7
 };
-constexpr TileShape kTiles[] = {{64, 16, 1, 0}, {256, 256, 1, 1.3f}, {128, 128, 2, 1.0f}, {64, 128, 2, 0.8f}, {64, 32, 2, 0.5f}};
+struct TileShape {
+    int tm, tn, per_cu;
+    float fixed, stage1, stage2;
+};
+constexpr TileShape kTiles[] = {{64, 16, 1, 0, 0, 0},
+                                {256, 256, 1, 10.0f, 1.40f, 1.40f},
+                                {128, 128, 2, 8.0f, 0.78f, 1.00f},
+                                {64, 128, 2, 6.5f, 0.41f, 0.70f},
+                                {64, 32, 2, 7.0f, 0.25f, 0.35f},
+                                {128, 128, 1, 8.0f, 0.54f, 0.54f},
+                                {64, 128, 1, 6.8f, 0.40f, 0.40f},
+                                {32, 128, 1, 6.5f, 0.36f, 0.36f}};
+constexpr int kCus = 256;
+constexpr float kJoin = 3.2f, kPartialRate = 5e6f;      // us of the join's launch; bytes a us of partial sums
 
 template <bool ALA, bool ALB, int TM, int TN, int WM, int WN, int WK, int NS>
 hipError_t launch_tile(const LinearParams &p, hipStream_t s)
@@ -1170,6 +1172,10 @@ hipError_t launch_op(const LinearParams &p, int tile, hipStream_t s)
     switch (tile) {
     case kTile256: return launch_wide<ALA, ALB>(p, s);
     case kTile128: return launch_tile<ALA, ALB, 128, 128, 2, 2, 1, 2>(p, s);
+    case kTile128Deep: return launch_tile<ALA, ALB, 128, 128, 2, 2, 1, 4>(p, s);
+    case kTile64Deep: return launch_tile<ALA, ALB, 64, 128, 2, 2, 1, 6>(p, s);
+    case kTile32Deep:
+        if constexpr (ALA) return launch_tile<ALA, ALB, 32, 128, 1, 2, 1, 7>(p, s);
     default: return launch_tile<ALA, ALB, 64, 128, 2, 2, 1, 3>(p, s);
     }
 }
@@ -1179,33 +1185,38 @@ hipError_t launch_few(const LinearParams &p, hipStream_t s)
     const bool glu = p.f.finish == kFinFwdGlu;
     const int64_t grid = ((glu ? p.N / 2 : p.N) + (glu ? 7 : 15)) / (glu ? 8 : 16);
     const dim3 g((unsigned)grid), b(kFewWaves * kWave);
-    if (p.M <= 16) hipLaunchKernelGGL(linear_few_kernel<1>, g, b, 0, s, p);
-    else if (p.M <= 32) hipLaunchKernelGGL(linear_few_kernel<2>, g, b, 0, s, p);
-    else hipLaunchKernelGGL(linear_few_kernel<4>, g, b, 0, s, p);
+    hipLaunchKernelGGL(linear_few_kernel, g, b, 0, s, p);
     return hipGetLastError();
 }
 
 }  // namespace
 
+// Up to 16 rows w streams through the few-row kernel (1 x 4096 x 4096: 10.5 us, 12.7
+// by tiles; 16: 13.3 and 13.3; 32: 16.7 and 14.0).  Else the tile and the parts of
+// the reduction whose cost by the table above is least.
 LinearPlan linear_plan(int op, int64_t M, int64_t N, int64_t K)
 {
     LinearPlan best = {kTileFew, 1, (K + kStage - 1) / kStage * kStage, 0};
-    if (op == kLinFwd && M <= 64) return best;
-    const int64_t stages = (K + kStage - 1) / kStage;
+    if (op == kLinFwd && M <= 16) return best;
+    const int stages = (int)((K + kStage - 1) / kStage);                  // at most 2^17
     float cost = 0;
-    for (int t = kTile256; t <= kTileNarrow; ++t) {
+    for (int t = kTile256; t <= kTile32Deep; ++t) {
         const TileShape &sh = kTiles[t];
-        if (t == kTileNarrow && (op != kLinFwd || N > 32)) continue;
-        const int64_t tiles = ((M + sh.tm - 1) / sh.tm) * ((N + sh.tn - 1) / sh.tn);
-        for (int want = 1; want <= 32 && (want == 1 || stages / want >= 4); want *= 2) {
-            const int64_t per = stages > 0 ? (stages + want - 1) / want : 1, splits = stages > 0 ? (stages + per - 1) / per : 1;
-            if (want > 1 && tiles * splits > 2048) break;
-            const int64_t rounds = (tiles * splits + 256 * sh.per_cu - 1) / (256 * sh.per_cu);
-            float c = (float)rounds * ((float)per * sh.stage + 3.0f);
-            if (splits > 1) c += 3.0f + (float)(splits * M * N) * (8.0f / 4e6f);
+        if (t == kTileNarrow ? op != kLinFwd || N > 32 : t == kTile32Deep && op == kLinWgrad) continue;
+        const int64_t all = ((M + sh.tm - 1) / sh.tm) * ((N + sh.tn - 1) / sh.tn);
+        if (t != kTile256 && all > (1 << 22)) continue;                  // a launch holds 2^32 threads
+        const int tiles = (int)all, full = kCus * sh.per_cu;
+        for (const int want : {1, 2, 3, 4, 5, 6, 8, 12, 16, 24, 32, 64}) {
+            if (want > 1 && (tiles > 4 * kCus / want || stages < 2 * want)) break;
+            const int per = stages > 0 ? (stages + want - 1) / want : 1, splits = stages > 0 ? (stages + per - 1) / per : 1;
+            const int wgs = tiles * splits, rounds = wgs / full, rest = wgs - rounds * full;
+            float c = (float)rounds * sh.stage2;
+            if (rest) c += rest <= kCus ? sh.stage1 : sh.stage2;
+            c = c * (float)per + sh.fixed;
+            if (splits > 1) c += kJoin + (float)splits * ((float)(M * N) * (8.0f / kPartialRate) + 0.15f);
             if (cost == 0 || c < cost) {
                 cost = c;
-                best = {t, (int)splits, per * kStage, splits > 1 ? splits * M * N * 4 : 0};
+                best = {t, splits, (int64_t)per * kStage, splits > 1 ? splits * M * N * 4 : 0};
             }
         }
     }

@@ -187,7 +187,7 @@ def test_workspace_sizes():
         assert pt.pt_linear_workspace_size(op, 0, 64, 64) == 0
     assert pt.pt_linear_workspace_size(3, 10, 64, 64) == 0
     # a few rows and products that fill the chip are not cut
-    assert pt.pt_linear_workspace_size(FWD, 1, 4096, 4096) == 0 and pt.pt_linear_workspace_size(FWD, 64, 8192, 8192) == 0
+    assert pt.pt_linear_workspace_size(FWD, 1, 4096, 4096) == 0 and pt.pt_linear_workspace_size(FWD, 16, 8192, 8192) == 0
     assert pt.pt_linear_workspace_size(FWD, 16384, 8192, 4096) == 0
     # fp32 sums of every part elsewhere: a whole number of products
     n = pt.pt_linear_workspace_size(DGRAD, 100, 4096, 264)
