@@ -28,7 +28,7 @@ namespace {
 // Traffic from which a call's rows go past the caches.
 constexpr int64_t kBlockStreamBytes = (int64_t)80 << 20;
 
-__host__ __device__ constexpr int team_threads(int W) { return W > 4 ? 64 * W : kThreads; }
+__host__ __device__ constexpr int team_threads(int W) { return W > 1 ? 64 * W : kThreads; }
 
 // The gate's bf16 values of row r (element base of the matrix), or null where it
 // is one number a row.  Chosen once per row: one address for both layouts.
@@ -193,35 +193,50 @@ hipError_t launch_fwd(const BlockNormFwdParams &p, hipStream_t s)
 }
 
 // ------------------------------------------------------------------ norms backward
-// The loads of a row's share as they come, so that the next row's can be in
+// What the call has, known when the kernel is compiled where it is all there: a
+// branch on each operand costs registers that the rows in flight need (16384 x 2880
+// with a gate per channel: 146 us, 129 without them).
+template <int GATE>
+struct Has {
+    static constexpr bool ALL = GATE >= 0;
+    const BlockNormBwdParams &p;
+    __device__ __forceinline__ bool pre() const { return ALL || p.pre; }
+    __device__ __forceinline__ bool post() const { return ALL || p.post; }
+    __device__ __forceinline__ bool dres() const { return ALL || p.dres; }
+    __device__ __forceinline__ int gate() const { return ALL ? GATE : p.gate_kind; }
+};
+
+// The loads of a row's share as they come, so that the next rows' can be in
 // flight while this one is worked on.
-template <bool F32, int TEAM, int NV, bool NT>
+template <bool F32, int GATE, int TEAM, int NV, bool NT>
 struct BlockRow {
     static constexpr int SV = F32 ? 2 : 1;               // 16-byte loads per 8 stream values
-    uintx4 dy[NV], x[NV], gate[NV], s[NV * SV], dres[NV * SV];
+    static constexpr bool MAY_FULL = GATE < 0 || GATE == kGateFull;
+    uintx4 dy[NV], x[NV], gate[MAY_FULL ? NV : 1], s[NV * SV], dres[NV * SV];
     float rpost, rpre, row_gate;
     __device__ __forceinline__ void load(const BlockNormBwdParams &p, int64_t r, int t)
     {
+        const Has<GATE> has{p};
         const int64_t base = r * p.cols;
-        rpost = p.post ? p.rstd_post[r] : 1.0f;
-        rpre = p.pre ? p.rstd_pre[r] : 1.0f;
-        row_gate = p.gate_kind == kGateRows ? ((const float *)p.gate)[r] : 1.0f;
+        rpost = has.post() ? p.rstd_post[r] : 1.0f;
+        rpre = has.pre() ? p.rstd_pre[r] : 1.0f;
+        row_gate = has.gate() == kGateRows ? ((const float *)p.gate)[r] : 1.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int e = (i * TEAM + t) * 8;
             if (e < p.cols) {
                 const int64_t at = (base + e) * (F32 ? 4 : 2);
                 x[i] = load_as<NT, uintx4>(p.x + base + e);
-                if (p.pre) {
+                if (has.pre()) {
                     dy[i] = load_as<NT, uintx4>(p.dy + base + e);
 #pragma unroll
                     for (int j = 0; j < SV; ++j) s[i * SV + j] = load_as<NT && !F32, uintx4>((const uint8_t *)p.s + at + 16 * j);
                 }
-                if (p.dres) {
+                if (has.dres()) {
 #pragma unroll
                     for (int j = 0; j < SV; ++j) dres[i * SV + j] = load_as<NT && !F32, uintx4>((const uint8_t *)p.dres + at + 16 * j);
                 }
-                if (p.gate_kind == kGateFull) gate[i] = load_as<NT, uintx4>((const uint16_t *)p.gate + base + e);
+                if (MAY_FULL && has.gate() == kGateFull) gate[MAY_FULL ? i : 0] = load_as<NT, uintx4>((const uint16_t *)p.gate + base + e);
             }
         }
     }
@@ -239,34 +254,28 @@ struct BlockRow {
 // W waves hold a row; a workgroup's teams take rows a grid apart and keep their
 // lanes' two sums over rows in registers: a = dwpre, b = dwpost, or for a gate
 // per column sum t.  The teams' are added in order, the workgroups' by
-// block_norm_join_kernel.
-template <bool F32, int W, int NV, bool NT>
+// block_norm_join_kernel.  The loads of the next two rows are in flight while one
+// is worked on.
+template <bool F32, int GATE, int W, int NV, bool NT>
 __global__ __launch_bounds__(team_threads(W)) void block_norm_bwd_kernel(BlockNormBwdParams p, int parts)
 {
     constexpr int TEAM = 64 * W, TEAMS = team_threads(W) / TEAM;
     __shared__ float s_sum[6][W];
     __shared__ floatx4 s_acc[TEAMS > 1 ? (TEAMS - 1) * TEAM * NV * 4 : 1];
+    const Has<GATE> has{p};
     const int t = (int)threadIdx.x % TEAM, team = (int)threadIdx.x / TEAM;
     float a[NV][8] = {}, b[NV][8] = {};
     int flip = 0;
-    const uint16_t *col_gate = p.gate_kind == kGateCols ? (const uint16_t *)p.gate : nullptr;
+    const uint16_t *col_gate = has.gate() == kGateCols ? (const uint16_t *)p.gate : nullptr;
     const int64_t first = (int64_t)blockIdx.x * TEAMS + team, step = (int64_t)parts * TEAMS;
-    constexpr bool AHEAD = NV <= 2;                      // longer shares fill the registers
-    BlockRow<F32, TEAM, NV, NT> next;
-    if (AHEAD && first < p.rows) next.load(p, first, t);
-    for (int64_t r = first; r < p.rows; r += step, flip ^= 3) {
+    using Row = BlockRow<F32, GATE, TEAM, NV, NT>;
+    constexpr int AHEAD = NV > 1 || GATE < 0 ? 0 : F32 || GATE == kGateFull ? 1 : 2;     // what the registers hold
+    auto work = [&](const Row &row, int64_t r) {
         const int64_t base = r * p.cols;
-        BlockRow<F32, TEAM, NV, NT> row;
-        if constexpr (AHEAD) {
-            row = next;
-            if (r + step < p.rows) next.load(p, r + step, t);
-        } else {
-            row.load(p, r, t);
-        }
         float ds[NV][8];
         // ds = dres + rpre (g - h c)
         float c = 0.0f;
-        if (p.pre) {
+        if (has.pre()) {
             float dot = 0.0f;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
@@ -296,8 +305,8 @@ __global__ __launch_bounds__(team_threads(W)) void block_norm_bwd_kernel(BlockNo
             const int e = (i * TEAM + t) * 8;
             if (e < p.cols) {
                 float x[8], w[8], k[8], d[8] = {}, o[8], dg[8];
-                if (p.dres) row.widen(row.dres + i * row.SV, d);
-                if (p.pre) {
+                if (has.dres()) row.widen(row.dres + i * row.SV, d);
+                if (has.pre()) {
                     float h[8];
                     row.widen(row.s + i * row.SV, h);
 #pragma unroll
@@ -307,9 +316,9 @@ __global__ __launch_bounds__(team_threads(W)) void block_norm_bwd_kernel(BlockNo
                 for (int j = 0; j < 8; ++j) o[j] = p.residual_scale * d[j], d[j] *= p.branch_scale;
                 store_stream<F32, NT>(p.dresidual, base + e, o);
                 unpack8(row.x[i], x);
-                if (p.gate_kind == kGateFull) unpack8(row.gate[i], k);
+                if (Row::MAY_FULL && has.gate() == kGateFull) unpack8(row.gate[Row::MAY_FULL ? i : 0], k);
                 else gate8(col_gate, e, row.row_gate, k);
-                if (p.post) unpack8(*(const uintx4 *)(p.post + e), w);
+                if (has.post()) unpack8(*(const uintx4 *)(p.post + e), w);
                 else {
 #pragma unroll
                     for (int j = 0; j < 8; ++j) w[j] = 1.0f;
@@ -318,23 +327,23 @@ __global__ __launch_bounds__(team_threads(W)) void block_norm_bwd_kernel(BlockNo
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const float tt = d[j] * (x[j] * row.rpost);
-                    b[i][j] += p.gate_kind == kGateCols ? tt : tt * k[j];
+                    b[i][j] += has.gate() == kGateCols ? tt : tt * k[j];
                     dg[j] = tt * w[j];
                     gpart += dg[j];
                     ds[i][j] = d[j] * k[j] * w[j];
                     part = __builtin_fmaf(ds[i][j], x[j], part);
                 }
-                if (p.gate_kind == kGateFull && p.dgate) store_as<NT>((uint16_t *)p.dgate + base + e, pack8(dg));
+                if (has.gate() == kGateFull && p.dgate) store_as<NT>((uint16_t *)p.dgate + base + e, pack8(dg));
                 dot += part;
                 gsum += gpart;
             }
         }
         float c2 = 0.0f;
-        if (p.post) {
+        if (has.post()) {
             dot = team_sum<W>(dot, s_sum[flip + 1]);
             c2 = row.rpost * row.rpost * (dot / (float)p.cols);
         }
-        if (p.gate_kind == kGateRows && p.dgate) {
+        if (has.gate() == kGateRows && p.dgate) {
             gsum = team_sum<W>(gsum, s_sum[flip + 2]);
             if (t == 0) ((float *)p.dgate)[r] = gsum;
         }
@@ -348,6 +357,25 @@ __global__ __launch_bounds__(team_threads(W)) void block_norm_bwd_kernel(BlockNo
                 for (int j = 0; j < 8; ++j) o[j] = row.rpost * (ds[i][j] - x[j] * c2);
                 store_as<NT>(p.dx + base + e, pack8(o));
             }
+        }
+        flip ^= 3;                       // the next row's sums never meet readers of this one's
+    };
+    if constexpr (AHEAD == 0) {
+        for (int64_t r = first; r < p.rows; r += step) {
+            Row row;
+            row.load(p, r, t);
+            work(row, r);
+        }
+    } else {
+        Row next[AHEAD];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i)
+            if (first + i * step < p.rows) next[i].load(p, first + i * step, t);
+        for (int64_t r = first; r < p.rows; r += step) {
+            const Row row = next[0];
+            if (AHEAD > 1) next[0] = next[AHEAD - 1];
+            if (r + AHEAD * step < p.rows) next[AHEAD - 1].load(p, r + AHEAD * step, t);
+            work(row, r);
         }
     }
     if (!p.sums) return;
@@ -428,33 +456,51 @@ __global__ __launch_bounds__(kJoinThreads) void block_norm_join_kernel(BlockNorm
     if (cols && p.dgate) put4((float *)p.dgate, c, p.post ? sum * widen4(p.post + c) : sum, p.accumulate);
 }
 
-template <bool F32, bool NT>
-hipError_t launch_bwd_as(const BlockNormBwdParams &p, hipStream_t s)
+// Waves of a row in the backward: 8 columns a lane, which leaves registers for the
+// loads of two rows more (8192 x 4096 bf16: 90 us, 99 with 16 a lane and one row).
+int bwd_waves(int64_t cols) { const int64_t n8 = cols / 8; return n8 <= 64 ? 1 : n8 <= 128 ? 2 : n8 <= 256 ? 4 : n8 <= 512 ? 8 : 16; }
+
+template <bool F32, int GATE, bool NT>
+void launch_bwd_rows(const BlockNormBwdParams &p, int parts, hipStream_t s)
 {
-    const int n8 = p.cols / 8, parts = block_norm_parts(p.rows);
-#define PTGG_NORM(W, NV)                                                                                              \
-    hipLaunchKernelGGL((block_norm_bwd_kernel<F32, W, NV, NT>), dim3((unsigned)parts), dim3(team_threads(W)), 0, s, p, \
+#define PTGG_NORM(W, NV)                                                                                                   \
+    hipLaunchKernelGGL((block_norm_bwd_kernel<F32, GATE, W, NV, NT>), dim3((unsigned)parts), dim3(team_threads(W)), 0, s, p, \
                        parts)
-    if (p.rows > 0) {
-        if (n8 <= 64) PTGG_NORM(1, 1);
-        else if (n8 <= 128) PTGG_NORM(1, 2);
-        else if (n8 <= 256) PTGG_NORM(4, 1);
-        else if (n8 <= 512) PTGG_NORM(4, 2);
-        else if (n8 <= 1024) PTGG_NORM(8, 2);
-        else PTGG_NORM(8, 4);
+    switch (bwd_waves(p.cols)) {
+    case 1: PTGG_NORM(1, 1); break;
+    case 2: PTGG_NORM(2, 1); break;
+    case 4: PTGG_NORM(4, 1); break;
+    case 8: PTGG_NORM(8, 1); break;
+    default:
+        if (p.cols <= 8192) PTGG_NORM(16, 1);
+        else PTGG_NORM(16, 2);
     }
 #undef PTGG_NORM
-    if (p.sums)
-        hipLaunchKernelGGL(block_norm_join_kernel, dim3((unsigned)((p.cols + kJoinCols - 1) / kJoinCols), 2),
-                           dim3(kJoinThreads), 0, s, p, p.rows > 0 ? parts : 0);
-    return hipGetLastError();
+}
+
+template <bool F32, bool NT>
+void launch_bwd_gate(const BlockNormBwdParams &p, int parts, hipStream_t s)
+{
+    if (!p.pre || !p.post || !p.dres) launch_bwd_rows<F32, -1, false>(p, parts, s);
+    else if (p.gate_kind == kGateNone) launch_bwd_rows<F32, kGateNone, NT>(p, parts, s);
+    else if (p.gate_kind == kGateCols) launch_bwd_rows<F32, kGateCols, NT>(p, parts, s);
+    else if (p.gate_kind == kGateRows) launch_bwd_rows<F32, kGateRows, NT>(p, parts, s);
+    else launch_bwd_rows<F32, kGateFull, NT>(p, parts, s);
 }
 
 template <bool F32>
 hipError_t launch_bwd(const BlockNormBwdParams &p, hipStream_t s)
 {
-    const int64_t bytes = p.rows * p.cols * (F32 ? 18 : 12);
-    return bytes > kBlockStreamBytes ? launch_bwd_as<F32, true>(p, s) : launch_bwd_as<F32, false>(p, s);
+    const int parts = block_norm_parts(p.rows, p.cols);
+    if (p.rows > 0) {
+        const int64_t bytes = p.rows * p.cols * (F32 ? 18 : 12);
+        if (bytes > kBlockStreamBytes) launch_bwd_gate<F32, true>(p, parts, s);
+        else launch_bwd_gate<F32, false>(p, parts, s);
+    }
+    if (p.sums)
+        hipLaunchKernelGGL(block_norm_join_kernel, dim3((unsigned)((p.cols + kJoinCols - 1) / kJoinCols), 2),
+                           dim3(kJoinThreads), 0, s, p, p.rows > 0 ? parts : 0);
+    return hipGetLastError();
 }
 
 // ------------------------------------------------------------------ experts' weighted sum
@@ -586,9 +632,10 @@ hipError_t launch_block_norm_fwd(const BlockNormFwdParams &p, hipStream_t s)
     }
 }
 
-int block_norm_parts(int64_t rows)
+// As many workgroups as the card holds at once: each writes two rows of sums.
+int block_norm_parts(int64_t rows, int64_t cols)
 {
-    const int64_t most = rows < 1024 ? 256 : rows < 4096 ? 512 : 1024;
+    const int waves = bwd_waves(cols), most = waves > 1 ? 4096 / waves : 1024;
     return (int)(rows < 1 ? 1 : rows < most ? rows : most);
 }
 

@@ -111,7 +111,7 @@ struct BlockNormBwdParams {
     int accumulate;
     int sums;                 // dpre, dpost or a gate per column's gradient is wanted
 };
-int block_norm_parts(int64_t rows);
+int block_norm_parts(int64_t rows, int64_t cols);
 hipError_t launch_block_norm_bwd(const BlockNormBwdParams &p, hipStream_t s);
 
 // ------------------------------------------------------------------ experts' weighted sum

@@ -202,7 +202,7 @@ int pt_linear_act_bwd(const void *dout, const void *c, void *dc, int64_t M, int6
 size_t pt_block_norm_workspace_size(int64_t rows, int64_t cols)
 {
     if (rows <= 0 || cols <= 0 || rows > kMaxRows || cols > kBlockMaxCols) return 0;
-    return (size_t)block_norm_parts(rows) * 2 * (size_t)cols * 4;
+    return (size_t)block_norm_parts(rows, cols) * 2 * (size_t)cols * 4;
 }
 
 int pt_block_norm_fwd(const void *x, const void *residual, const void *post_weight, const void *gate,
