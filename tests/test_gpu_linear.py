@@ -149,6 +149,59 @@ def test_swiglu_pairs_exact(dev, M, N, K):
     assert torch.equal(forward(x, w, bias, act="swiglu", out_type=F32), want.to(F32))
 
 
+# sizes at which the rules take each tile, whole and with the reduction in parts
+FWD_TILES = [(5857, 5040, 72), (5724, 672, 3064), (6863, 4496, 8), (5666, 272, 3896), (4189, 144, 8), (1270, 16, 1320), (18, 16, 264),
+             (19, 16, 2200), (5925, 272, 632), (4374, 48, 3752), (4376, 144, 1944), (155, 4368, 4120), (19, 16, 1224)]
+DGRAD_TILES = [(6311, 72, 4808), (5808, 3144, 664), (6797, 8, 4528), (4289, 4712, 8), (4170, 8, 144), (1436, 1048, 8), (5925, 600, 264),
+               (3382, 4624, 8), (4448, 1976, 152), (290, 3904, 2464), (19, 840, 8)]
+WGRAD_TILES = [(202, 3800, 3208), (7541, 4240, 392), (80, 3784, 3840), (5423, 4272, 8), (778, 8, 8), (612, 4144, 392), (3591, 4368, 8),
+               (2272, 4744, 152), (8098, 136, 2528)]
+
+
+@pytest.mark.parametrize("M,N,K", FWD_TILES)
+def test_forward_exact_in_every_tile(dev, M, N, K):
+    g = gen(dev, M + N + K)
+    x, w, bias = ints(g, M, K), ints(g, N, K), ints(g, N, top=20)
+    c = x.to(F64) @ w.to(F64).t() + bias.to(F64)
+    out, saved = forward(x, w, bias, out_type=F32, save=True)
+    assert torch.equal(out, c.to(F32)) and torch.equal(saved, c.to(BF16))
+    I = N // 2
+    w[:I] = 0
+    bias[:I] = (128 + torch.arange(I, device=dev) % 64).to(BF16)
+    want = bias[:I].to(F64) * (x.to(F64) @ w[I:].to(F64).t() + bias[I:].to(F64))
+    assert want.abs().max() < 2 ** 24
+    out, saved = forward(x, w, bias, act="swiglu", out_type=F32, save=True)
+    assert torch.equal(out, want.to(F32))
+    assert torch.equal(saved[:, I:], (x.to(F64) @ w[I:].to(F64).t() + bias[I:].to(F64)).to(BF16))
+
+
+@pytest.mark.parametrize("M,N,K", DGRAD_TILES)
+def test_dgrad_exact_in_every_tile(dev, M, N, K):
+    g = gen(dev, M + N + K + 1)
+    dy, w = ints(g, M, N), ints(g, N, K)
+    dh = dy.to(F64) @ w.to(F64)
+    assert torch.equal(dgrad(dy, w), dh.to(BF16))
+    # gates at which silu is the identity and its slope 1: both gradients are exact
+    c = torch.empty((M, 2 * K), dtype=BF16, device=dev)
+    c[:, :K] = (128 + torch.arange(K, device=dev) % 64).to(BF16)
+    c[:, K:] = ints(g, M, K)
+    got = dgrad(dy, w, c, act="swiglu")
+    assert torch.equal(got[:, :K], (dh * c[:, K:].to(F64)).to(BF16))
+    assert torch.equal(got[:, K:], (dh * c[:, :K].to(F64)).float().to(BF16))
+
+
+@pytest.mark.parametrize("M,N,K", WGRAD_TILES)
+def test_wgrad_exact_in_every_tile(dev, M, N, K):
+    g = gen(dev, M + N + K + 2)
+    x, dy = ints(g, M, K), ints(g, M, N)
+    dw, db = dy.to(F64).t() @ x.to(F64), dy.to(F64).sum(0)
+    start, startb = ints(g, N, K, top=50).float(), ints(g, N, top=50).float()
+    got, gotb = wgrad(x, dy)
+    assert torch.equal(got, dw.to(F32)) and torch.equal(gotb, db.to(F32))
+    got, gotb = wgrad(x, dy, accumulate=1, main_grad=start.clone(), dbias=startb.clone())
+    assert torch.equal(got, (dw + start.to(F64)).to(F32)) and torch.equal(gotb, (db + startb.to(F64)).to(F32))
+
+
 def sums(x, w, bias):
     """c in 64 bits and what it may be off by."""
     c = x.to(F64) @ w.to(F64).t()
