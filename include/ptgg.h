@@ -830,8 +830,8 @@ size_t pt_linear_workspace_size(int op, int64_t M, int64_t N, int64_t K);
  *  rstd_post, rstd_pre  [rows] fp32 for the backward, or NULL
  * Rows of zeros, NaN and infinities as pt_rmsnorm_fwd.
  *  Requirements: cols % 8 == 0 (cols % 32 == 0 for MXFP8), cols <= 16384,
- *  rows <= 2^23, eps >= 0; matrices, weights and gate 16-byte aligned (a gate per
- *  row 4-byte).
+ *  rows <= 2^23, rows cols <= 2^36, eps >= 0; matrices, weights and gate 16-byte
+ *  aligned (a gate per row 4-byte).
  */
 int pt_block_norm_fwd(const void *x, const void *residual, const void *post_weight, const void *gate,
                       const void *pre_weight, void *residual_out, void *y, void *q, void *scales, float *rstd_post,
@@ -881,8 +881,8 @@ size_t pt_block_norm_workspace_size(int64_t rows, int64_t cols);
  *           and its weight is not read
  *  base     [T, H] bf16: a shared expert's output, or NULL; may be out itself
  *  out      [T, H] bf16
- *  Requirements: H % 8 == 0, H <= 32768, k <= PT_MAX_TOPK, T <= 2^23, M < 2^31;
- *  rows, base and out 16-byte aligned.
+ *  Requirements: H % 8 == 0, H <= 32768, k <= PT_MAX_TOPK, T <= 2^23, T H <= 2^36,
+ *  M < 2^31; rows, base and out 16-byte aligned.
  */
 int pt_moe_combine(const void *rows, const float *weights, const int32_t *row_of, const void *base, void *out, int64_t T,
                    int64_t M, int64_t H, int64_t k, void *stream);
@@ -894,8 +894,8 @@ int pt_moe_combine(const void *rows, const float *weights, const int32_t *row_of
  * Without weights and dweights it is the gather A[row_of[t, j]] = x[t] of the
  * experts' operand, each row of x read once.
  *  drows    [M, H] bf16, or NULL; rows that no slot names are left as they are.  A
- *           row is named once, as pt_moe_route does: of two slots that name the
- *           same row one is written
+ *           row is named once, as pt_moe_route does: where two slots name the same
+ *           row each of its elements is one slot's or the other's
  *  dweights [T, k] fp32, or NULL; 0 for a slot without a row
  *  rows     [M, H] bf16: needed for dweights, else NULL
  *  Requirements as pt_moe_combine; dout and drows 16-byte aligned.

@@ -12,6 +12,7 @@ namespace {
 
 constexpr int64_t kMaxWidth = (int64_t)1 << 17;          // columns and reduction of a product
 constexpr int64_t kMaxProduct = (int64_t)1 << 38;        // elements of a matrix
+constexpr int64_t kMaxTokens = (int64_t)1 << 36;         // elements of a matrix of rows: a launch stays below 2^32 threads
 
 bool is_act(int act) { return act >= PT_ACT_NONE && act <= PT_ACT_SWIGLU; }
 
@@ -48,14 +49,15 @@ int check_block_norm(int64_t rows, int64_t cols, float branch_scale, float resid
     if (rows < 0 || cols < 1 || branch_scale != branch_scale || residual_scale != residual_scale) return PT_ERR_INVALID_ARG;
     if (gate_kind < PT_BLOCK_GATE_NONE || gate_kind > PT_BLOCK_GATE_FULL) return PT_ERR_INVALID_ARG;
     if (stream_dtype != PT_BF16 && stream_dtype != PT_FP32) return PT_ERR_UNSUPPORTED;
-    if (cols % 8 || cols > kBlockMaxCols || rows > kMaxRows) return PT_ERR_UNSUPPORTED;
+    if (cols % 8 || cols > kBlockMaxCols || rows > kMaxRows || rows * cols > kMaxTokens) return PT_ERR_UNSUPPORTED;
     return PT_OK;
 }
 
 int check_combine(int64_t T, int64_t M, int64_t H, int64_t k)
 {
     if (T < 0 || M < 0 || H < 1 || k < 1) return PT_ERR_INVALID_ARG;
-    if (H % 8 || H > kCombineMaxCols || k > PT_MAX_TOPK || T > kMaxRows || M > INT32_MAX) return PT_ERR_UNSUPPORTED;
+    if (H % 8 || H > kCombineMaxCols || k > PT_MAX_TOPK || T > kMaxRows || M > INT32_MAX || T * H > kMaxTokens)
+        return PT_ERR_UNSUPPORTED;
     return PT_OK;
 }
 
@@ -68,7 +70,7 @@ size_t pt_linear_workspace_size(int op, int64_t M, int64_t N, int64_t K)
     if ((op != PT_OP_FWD && op != PT_OP_DGRAD && op != PT_OP_WGRAD) || check_product(M, N, K) != PT_OK) return 0;
     if (M == 0) return 0;
     const LinearPlan plan = plan_of(op, M, N, K);
-    return (size_t)(round256(plan.partial_bytes) + (op == PT_OP_WGRAD ? colsum_bytes(M, N) : 0));
+    return (size_t)(plan.partial_bytes + (op == PT_OP_WGRAD ? colsum_bytes(M, N) : 0));
 }
 
 int pt_linear_fwd(const void *x, const void *w, const void *bias, const void *residual, void *out, void *c, int64_t M,
@@ -155,8 +157,7 @@ int pt_linear_wgrad(const void *x, const void *dy, float *main_grad, float *dbia
     if (!main_grad || (M > 0 && (!x || !dy))) return PT_ERR_INVALID_ARG;
     if (!aligned(x, 16) || !aligned(dy, 16) || !aligned(main_grad, 16) || !aligned(dbias, 16)) return PT_ERR_MISALIGNED;
     const LinearPlan plan = plan_of(PT_OP_WGRAD, M, N, K);
-    const int64_t sums = dbias && M > 0 ? colsum_bytes(M, N) : 0, at = round256(plan.partial_bytes);
-    const int64_t need = sums ? at + sums : plan.partial_bytes;
+    const int64_t at = plan.partial_bytes, need = at + (dbias && M > 0 ? colsum_bytes(M, N) : 0);
     if (need && (!workspace || workspace_bytes < (size_t)need)) return PT_ERR_WORKSPACE;
     if (need && !aligned(workspace, 16)) return PT_ERR_MISALIGNED;
     if (!device_is_gfx950()) return PT_ERR_UNSUPPORTED;
@@ -264,8 +265,10 @@ int pt_block_norm_bwd(const void *dy, const void *dres, const void *x, const voi
     // sums over rows: they are written also where there are no rows
     const bool sums = dpost || dpre || (dgate && gate_kind == PT_BLOCK_GATE_COLS);
     if (rows == 0 && (!sums || accumulate)) return PT_OK;
+    // the sums' last step reads the gate whatever the rows are
+    if ((gate != nullptr) != (gate_kind != PT_BLOCK_GATE_NONE)) return PT_ERR_INVALID_ARG;
     if (rows > 0) {
-        if (!x || !dx || !dresidual || (gate != nullptr) != (gate_kind != PT_BLOCK_GATE_NONE)) return PT_ERR_INVALID_ARG;
+        if (!x || !dx || !dresidual) return PT_ERR_INVALID_ARG;
         if (pre_weight ? !dy || !s || !rstd_pre : dy != nullptr) return PT_ERR_INVALID_ARG;
         if (!pre_weight && !dres) return PT_ERR_INVALID_ARG;        // no gradient comes in at all
         if (post_weight && !rstd_post) return PT_ERR_INVALID_ARG;

@@ -1100,7 +1100,7 @@ __global__ __launch_bounds__(kThreads) void colsum_join_kernel(const float *__re
 }
 
 template <int FIN>
-__global__ __launch_bounds__(kThreads) void act_bwd_kernel(const uint16_t *__restrict__ dout, FinishParams f, int64_t M)
+__global__ __launch_bounds__(kThreads) void act_bwd_kernel(const uint16_t *dout, FinishParams f, int64_t M)
 {
     const int64_t groups = f.N / 8, total = M * groups;
     for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kThreads) {

@@ -209,3 +209,19 @@ def test_binding_refuses_what_the_library_cannot_see():
     for bad in (t[:, :8], t.t(), t.cpu()):
         with pytest.raises(ValueError):
             pt.pt_linear_fwd(bad, t, None, None, t, None, 8, 8, 8)
+
+
+def test_no_rows_still_need_the_gate(L, buf):
+    """The gradients of weights that are written without rows: zeros times the gate, which has to be there."""
+    def f(kind, gate, ws=buf):
+        return L.pt_block_norm_bwd(None, None, None, None, buf, gate, buf, None, None, None, None, buf if kind else None, buf, buf,
+                                   0, 64, 1.0, 1.0, kind, 0, 0, ws, 1 << 20, None)
+    assert f(1, None) == INVALID and f(2, None) == INVALID and f(0, buf) == INVALID
+
+
+def test_most_elements(L, buf):
+    rows = 1 << 23
+    assert L.pt_block_norm_fwd(buf, buf, None, None, None, buf, None, None, None, None, None, rows, 8200, 1e-5, 1.0, 1.0, 0, 0, 0,
+                               None) == UNSUPPORTED
+    assert L.pt_moe_combine(buf, None, buf, None, buf, rows, 8, 8200, 1, None) == UNSUPPORTED
+    assert L.pt_moe_combine_bwd(buf, buf, None, buf, buf, None, rows, 8, 8200, 1, None) == UNSUPPORTED
