@@ -35,6 +35,16 @@ struct FinishParams {
     float limit;              // SwiGLU clamp, +inf for none
 };
 
+// How the widest tile's work is spread over the CUs (wide_cut in linear.hip): the
+// first `whole` tiles in one piece; each of the `rest` others in `parts` of `main`
+// reduction values and a tail, which the first `tails` of them take in one piece,
+// the others in `cuts` of `cut` values.  rest = 0: every tile in one piece.
+struct WideCut {
+    int whole, rest, parts, tails, cuts;
+    int64_t main, cut;
+    __host__ __device__ int pieces() const { return parts * rest + tails + (rest - tails) * cuts; }
+};
+
 // C[m, n] = sum over q < K of A(m, q) B(n, q): forward A = x, B = w; dgrad
 // A = dy, B = w by columns; wgrad A = dy and B = x by columns.
 struct LinearParams {
@@ -43,7 +53,8 @@ struct LinearParams {
     int64_t lda, ldb;         // elements between rows in memory
     int splits;               // parts of the reduction
     int64_t part;             // reduction values a part (a multiple of 64)
-    float *partials;          // workspace: splits x [M, N] fp32, where splits > 1
+    float *partials;          // workspace: splits x [M, N] fp32, where splits > 1; or the cut's pieces, a tile each
+    WideCut cut;              // of the widest tile
     FinishParams f;
 };
 
@@ -52,6 +63,7 @@ struct LinearPlan {
     int tile;
     int splits;
     int64_t part;
+    WideCut cut;
     int64_t partial_bytes;
 };
 LinearPlan linear_plan(int op, int64_t M, int64_t N, int64_t K);

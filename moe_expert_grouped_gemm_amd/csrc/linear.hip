@@ -508,10 +508,10 @@ struct Shape {
     static_assert(LDS <= (160 << 10) && (WK == 1 || WM * WN == 1), "LDS of a tile");
 };
 
-// Logical workgroup number: consecutive ones share an XCD and its L2.
-__device__ __forceinline__ uint32_t xcd_order()
+// Logical number of workgroup b of n: consecutive ones share an XCD and its L2.
+__device__ __forceinline__ uint32_t xcd_order(uint32_t b, uint32_t n)
 {
-    const uint32_t n = gridDim.x, b = blockIdx.x, q = n / 8, r = n % 8, x = b % 8;
+    const uint32_t q = n / 8, r = n % 8, x = b % 8;
     return x * q + min(x, r) + b / 8;
 }
 
@@ -546,7 +546,7 @@ __device__ __forceinline__ void put_rows(const floatx4 (&acc)[MI][NJ], int i, ui
 
 template <int FIN, bool F32, int MI, int NJ, int WK, class Acc>
 __device__ __forceinline__ void finish_wave_as(const LinearParams &p, const Acc &acc, uint8_t *lds, int wk, int64_t m0,
-                                               int64_t n0, int64_t split)
+                                               int64_t n0, float *partial, int64_t ldp)
 {
     constexpr int C = NJ * 32, PITCH = wave_pitch<C>();
     constexpr bool GLU = FIN == kFinFwdGlu;
@@ -612,9 +612,9 @@ __device__ __forceinline__ void finish_wave_as(const LinearParams &p, const Acc 
     };
     if (m0 >= p.M && WK == 1) return;
     if constexpr (FIN == kFinPartial) {
-        const uint8_t *out = (const uint8_t *)(p.partials + (split * p.M + m0) * p.N);
-        const uint32_t row_b = (uint32_t)p.N * 4, bytes = (uint32_t)max(min(p.M - m0, (int64_t)kWideRows), (int64_t)0) * row_b;
-        const uint32_t vo = n < ncols ? r0 * row_b + (uint32_t)n * 4 : kOOB;
+        const uint8_t *out = (const uint8_t *)partial;
+        const uint32_t row_b = (uint32_t)ldp * 4, bytes = (uint32_t)max(min(p.M - m0, (int64_t)kWideRows), (int64_t)0) * row_b;
+        const uint32_t vo = n < ldp ? r0 * row_b + (uint32_t)n * 4 : kOOB;
         all([&](auto, int row, float (&v)[8], float (&)[8]) {
             buf_store(uintx4{f32_bits(v[0]), f32_bits(v[1]), f32_bits(v[2]), f32_bits(v[3])}, out, bytes, vo, row * row_b);
             buf_store(uintx4{f32_bits(v[4]), f32_bits(v[5]), f32_bits(v[6]), f32_bits(v[7])}, out, bytes, vo, row * row_b + 16);
@@ -631,16 +631,18 @@ __device__ __forceinline__ void finish_wave_as(const LinearParams &p, const Acc 
     }
 }
 
-// OP: the operator, which says what there is to finish.
+// OP: the operator, which says what there is to finish.  in_parts: the sums are those
+// of a part of the reduction, and go to `partial`, the wave's first row there, whose
+// rows are ldp apart, from column n0 on.
 template <int OP, int MI, int NJ, int WK, class Acc>
 __device__ __forceinline__ void finish_wave(const LinearParams &p, const Acc &acc, uint8_t *lds, int wk, int64_t m0,
-                                            int64_t n0, int64_t split)
+                                            int64_t n0, bool in_parts, float *partial, int64_t ldp)
 {
     constexpr int PLAIN = OP == kLinDgrad ? kFinGrad : kFinFwd, GLU = OP == kLinDgrad ? kFinGradGlu : kFinFwdGlu;
     auto as = [&](auto F, auto F32) {
-        finish_wave_as<decltype(F)::value, decltype(F32)::value, MI, NJ, WK>(p, acc, lds, wk, m0, n0, split);
+        finish_wave_as<decltype(F)::value, decltype(F32)::value, MI, NJ, WK>(p, acc, lds, wk, m0, n0, partial, ldp);
     };
-    if (p.f.finish == kFinPartial) {
+    if (in_parts) {
         as(IC<kFinPartial>{}, IC<true>{});
     } else if (OP != kLinWgrad && p.f.finish == GLU) {
         if (OP == kLinFwd && p.f.f32) as(IC<GLU>{}, IC<OP == kLinFwd>{});
@@ -656,22 +658,20 @@ __device__ __forceinline__ void finish_wave(const LinearParams &p, const Acc &ac
 // operands' loads.
 template <bool ALA, bool ALB, int TM, int TN, int NT, int C>
 struct Place {
-    int64_t m0, n0, split;
+    int64_t m0, n0;
     int klen;
     bool glu;
     Operand<ALA, TM, NT, 0> a;
     Operand<ALB, TN, NT, ALB ? C / 2 : 0> b;             // a wave has C columns
 
-    __device__ __forceinline__ void init(const LinearParams &p, int tilesM, int tilesN)
+    // reduction values kb on, klen at most
+    __device__ __forceinline__ void init(const LinearParams &p, int tile, int tilesM, int tilesN, int64_t kb, int64_t len)
     {
-        const uint32_t id = xcd_order(), tiles = (uint32_t)tilesM * (uint32_t)tilesN;
-        split = id / tiles;
         int mt, nt;
-        grouped_tile_order((int)(id % tiles), tilesM, tilesN, mt, nt);
+        grouped_tile_order(tile, tilesM, tilesN, mt, nt);
         m0 = (int64_t)mt * TM;
         glu = p.f.finish == kFinFwdGlu;
-        const int64_t kb = split * p.part;
-        klen = (int)min(p.K - kb, p.part);
+        klen = (int)min(p.K - kb, len);
         // columns of the tile: n0 on; with SwiGLU, half as many gates and their ups, C / 2 of each to a wave
         n0 = (int64_t)nt * (glu ? TN / 2 : TN);
         const int64_t half = p.N >> 1;
@@ -699,8 +699,10 @@ __global__ __launch_bounds__(64 * WM * WN * WK, 2) void linear_kernel(LinearPara
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wk = wave % WK, wn = wave / WK % WN, wm = wave / WK / WN;
 
+    const uint32_t id = xcd_order(blockIdx.x, gridDim.x), tiles = (uint32_t)tilesM * (uint32_t)tilesN;
+    const int64_t split = id / tiles;
     Place<ALA, ALB, TM, TN, NT, NJ * 32> at;
-    at.init(p, tilesM, tilesN);
+    at.init(p, (int)(id % tiles), tilesM, tilesN, split * p.part, p.part);
     const uint32_t lds0 = lds_addr(smem);
     Frags<ALA, TM> ra;
     Frags<ALB, TN> rb;
@@ -795,7 +797,9 @@ __global__ __launch_bounds__(64 * WM * WN * WK, 2) void linear_kernel(LinearPara
     wait_vmcnt<0>();                             // zeros of stages past the end may still be landing in the ring
     barrier();
 
-    finish_wave<ALA ? ALB ? kLinFwd : kLinDgrad : kLinWgrad, MI, NJ, WK>(p, acc, smem + (WK > 1 ? 0 : wave * S::EPI), wk, at.m0 + wm * MI * 32, at.col(wn), at.split);
+    const int64_t m0 = at.m0 + wm * MI * 32;
+    finish_wave<ALA ? ALB ? kLinFwd : kLinDgrad : kLinWgrad, MI, NJ, WK>(p, acc, smem + (WK > 1 ? 0 : wave * S::EPI), wk, m0, at.col(wn), p.splits > 1,
+                                                                         p.partials + (split * p.M + m0) * p.N, p.N);
 }
 
 // ------------------------------------------------------------------ wide tile
@@ -852,8 +856,32 @@ __global__ __launch_bounds__(kWideThreads, 1) void linear_wide_kernel(LinearPara
     extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wn = wave & 1, wm = wave >> 1;
+    // this workgroup's piece of the work
+    const WideCut &cut = p.cut;
+    const int rest = cut.rest, left = rest - cut.tails, mains = cut.parts * rest;
+    int b = blockIdx.x, tile, slot = -1;
+    int64_t kb = 0, len = p.K;
+    if (b < cut.whole) {
+        tile = xcd_order(b, cut.whole);
+    } else if ((b -= cut.whole) < mains) {
+        slot = xcd_order(b, mains);
+        tile = cut.whole + slot % rest;
+        kb = slot / rest * cut.main;
+        len = cut.main;
+    } else if ((b -= mains) < cut.tails) {
+        const int t = xcd_order(b, cut.tails);
+        slot = mains + t;
+        tile = cut.whole + t;
+        kb = cut.parts * cut.main;
+    } else {
+        const int t = xcd_order(b - cut.tails, left * cut.cuts);
+        slot = mains + cut.tails + t;
+        tile = cut.whole + cut.tails + t % left;
+        kb = cut.parts * cut.main + t / left * cut.cut;
+        len = cut.cut;
+    }
     Place<ALA, ALB, kWide, kWide, kWideThreads, 128> at;
-    at.init(p, tilesM, tilesN);
+    at.init(p, tile, tilesM, tilesN, kb, len);
     const uint32_t lds0 = lds_addr(smem);
     uint8_t *const smem_b = smem + 3 * kWideSlot;
     WideFrags<ALA> ra;
@@ -920,7 +948,51 @@ __global__ __launch_bounds__(kWideThreads, 1) void linear_wide_kernel(LinearPara
     }
     wait_vmcnt<0>();                     // zeros of stages past the end may still be landing in the ring
     barrier();
-    finish_wave<ALA ? ALB ? kLinFwd : kLinDgrad : kLinWgrad, 4, 4, 1>(p, acc, smem + wave * 32 * wave_pitch<128>(), 0, at.m0 + wm * 128, at.col(wn), at.split);
+    // a piece's sums go to a tile of their own, its columns in the waves' order
+    finish_wave<ALA ? ALB ? kLinFwd : kLinDgrad : kLinWgrad, 4, 4, 1>(p, acc, smem + wave * 32 * wave_pitch<128>(), 0, at.m0 + wm * 128,
+                                                                     slot < 0 ? at.col(wn) : wn * 128, slot >= 0,
+                                                                     p.partials + ((int64_t)slot * kWide + wm * 128) * kWide, kWide);
+}
+
+// The pieces of a cut tile added in their order along the reduction, then what the
+// tile itself would have done.  A workgroup takes 8 rows (SwiGLU: 16), a thread 8 columns.
+template <int FIN>
+__global__ __launch_bounds__(kThreads) void linear_wide_join_kernel(LinearParams p, int tilesM, int tilesN)
+{
+    constexpr bool GLU = FIN == kFinFwdGlu;
+    constexpr int GROUPS = kWide / (GLU ? 16 : 8), ROWS = kThreads / GROUPS;
+    const WideCut &cut = p.cut;
+    const int t = blockIdx.x / (kWide / ROWS), g = threadIdx.x % GROUPS;
+    const int row = blockIdx.x % (kWide / ROWS) * ROWS + (int)threadIdx.x / GROUPS;
+    int mt, nt;
+    grouped_tile_order(cut.whole + t, tilesM, tilesN, mt, nt);
+    const int64_t m = (int64_t)mt * kWide + row, n = (int64_t)nt * (GLU ? kWide / 2 : kWide) + g * 8;
+    if (m >= p.M || n >= (GLU ? p.N >> 1 : p.N)) return;
+    // a wave's 128 columns are 64 gates and their ups
+    const float *src = p.partials + row * kWide + (GLU ? g / 8 * 128 + g % 8 * 8 : g * 8);
+    float v[8] = {}, u[8] = {};
+    auto add = [&](int slot) {
+        float f[8];
+        load_stream<true, false>(src, (int64_t)slot * kWide * kWide, f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] += f[j];
+        if (GLU) {
+            load_stream<true, false>(src, (int64_t)slot * kWide * kWide + 64, f);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) u[j] += f[j];
+        }
+    };
+    const int mains = cut.parts * cut.rest;
+#pragma unroll 4
+    for (int i = 0; i < cut.parts; ++i) add(i * cut.rest + t);
+    if (t < cut.tails) {
+        add(mains + t);
+    } else {
+        const int left = cut.rest - cut.tails;
+#pragma unroll 4
+        for (int i = 0; i < cut.cuts; ++i) add(mains + cut.tails + i * left + t - cut.tails);
+    }
+    finish_row<FIN>(p.f, m, n, v, u);
 }
 
 // ------------------------------------------------------------------ few rows
@@ -1160,9 +1232,14 @@ hipError_t launch_wide(const LinearParams &p, hipStream_t s)
     if (e != hipSuccess) return e;
     const bool glu = p.f.finish == kFinFwdGlu;
     const int64_t cols = glu ? p.N / 2 : p.N, tn = glu ? kWide / 2 : kWide;
-    const int64_t tilesM = (p.M + kWide - 1) / kWide, tilesN = (cols + tn - 1) / tn;
-    hipLaunchKernelGGL(kern, dim3((unsigned)(tilesM * tilesN * p.splits)), dim3(kWideThreads), kWideLds, s, p, (int)tilesM,
-                       (int)tilesN);
+    const int tilesM = (int)((p.M + kWide - 1) / kWide), tilesN = (int)((cols + tn - 1) / tn);
+    hipLaunchKernelGGL(kern, dim3((unsigned)(p.cut.whole + p.cut.pieces())), dim3(kWideThreads), kWideLds, s, p, tilesM, tilesN);
+    if (p.cut.rest) {
+        const dim3 g((unsigned)p.cut.rest * (glu ? 16 : 32)), b(kThreads);
+        constexpr int PLAIN = ALA && !ALB ? kFinGrad : kFinFwd, GLU = ALA && !ALB ? kFinGradGlu : kFinFwdGlu;
+        if (p.f.finish == GLU) hipLaunchKernelGGL(linear_wide_join_kernel<GLU>, g, b, 0, s, p, tilesM, tilesN);
+        else hipLaunchKernelGGL(linear_wide_join_kernel<PLAIN>, g, b, 0, s, p, tilesM, tilesN);
+    }
     return hipGetLastError();
 }
 
@@ -1189,6 +1266,49 @@ hipError_t launch_few(const LinearParams &p, hipStream_t s)
     return hipGetLastError();
 }
 
+// Tiles of the widest kind over the CUs, one to a CU at a time.  Whole tiles fill all
+// CUs some times over; the r that are left would keep r of them busy as long again.
+// So their reduction is cut: p = G / r parts a tile, and the e CUs that this leaves
+// take the tiles' tails, f of them one after another, and then what is left of the
+// tails in pieces: a tail is as long as lets both kinds of CUs end together.  Pieces
+// of a kind start at the same places of the reduction, so that an XCD's L2 serves
+// its tiles' common rows once.
+WideCut wide_cut(int tiles, int stages)
+{
+    constexpr float kPiece = 8.0f;                       // stages that a piece costs besides its own
+    WideCut cut = {tiles, 0, 0, 0, 0, 0, 0};
+    const int r = tiles % kCus;
+    if (r == 0) return cut;
+    const int fit = kCus / r, p = min(fit, max(stages / 8, 1)), e = p < fit ? 0 : kCus - p * r;
+    int tail = 0, f = 0, c = 1;
+    if (e > 0) {
+        f = r / e;
+        const int left = r - f * e;
+        c = left ? max(e / left, 1) : 1;
+        // main = slope tail + extra, stages = p main + tail
+        const float slope = (float)f + (left ? 1.0f / (float)c : 0.0f), extra = (float)(f + (left ? 1 : 0) - 1) * kPiece;
+        const float x = ((float)stages - (float)p * extra) / (1.0f + (float)p * slope);
+        tail = x >= 4.0f ? (int)x : 0;
+    }
+    const int main = (stages - tail + p - 1) / p;
+    tail = stages - p * main;
+    if (tail <= 0 && p == 1) return cut;
+    cut.whole = tiles - r;
+    cut.rest = r;
+    cut.main = (int64_t)main * kStage;
+    if (tail <= 0) {
+        cut.parts = (stages + main - 1) / main;
+        return cut;
+    }
+    cut.parts = p;
+    cut.tails = f * e;
+    c = min(c, max(tail / 8, 1));
+    const int piece = (tail + c - 1) / c;
+    cut.cuts = (tail + piece - 1) / piece;
+    cut.cut = (int64_t)piece * kStage;
+    return cut;
+}
+
 }  // namespace
 
 // Up to 16 rows w streams through the few-row kernel (1 x 4096 x 4096: 10.5 us, 12.7
@@ -1196,7 +1316,7 @@ hipError_t launch_few(const LinearParams &p, hipStream_t s)
 // the reduction whose cost by the table above is least.
 LinearPlan linear_plan(int op, int64_t M, int64_t N, int64_t K)
 {
-    LinearPlan best = {kTileFew, 1, (K + kStage - 1) / kStage * kStage, 0};
+    LinearPlan best = {kTileFew, 1, (K + kStage - 1) / kStage * kStage, {}, 0};
     if (op == kLinFwd && M <= 16) return best;
     const int stages = (int)((K + kStage - 1) / kStage);                  // at most 2^17
     float cost = 0;
@@ -1206,6 +1326,17 @@ LinearPlan linear_plan(int op, int64_t M, int64_t N, int64_t K)
         const int64_t all = ((M + sh.tm - 1) / sh.tm) * ((N + sh.tn - 1) / sh.tn);
         if (t != kTile256 && all > (1 << 22)) continue;                  // a launch holds 2^32 threads
         const int tiles = (int)all, full = kCus * sh.per_cu;
+        if (t == kTile256) {
+            const WideCut whole = {tiles, 0, 0, 0, 0, 0, 0}, cut = wide_cut(tiles, stages);
+            cost = (float)((tiles + kCus - 1) / kCus) * (float)stages * sh.stage1 + sh.fixed;
+            best = {t, 1, 0, whole, 0};
+            if (cut.rest) {
+                const float c = ((float)(tiles / kCus) * (float)stages + (float)(cut.main / kStage)) * sh.stage1 + sh.fixed + kJoin +
+                                (float)cut.pieces() * (kWide * kWide * 8.0f / kPartialRate);
+                if (c < cost) cost = c, best = {t, 1, 0, cut, (int64_t)cut.pieces() * kWide * kWide * 4};
+            }
+            continue;
+        }
         for (const int want : {1, 2, 3, 4, 5, 6, 8, 12, 16, 24, 32, 64}) {
             if (want > 1 && (tiles > 4 * kCus / want || stages < 2 * want)) break;
             const int per = stages > 0 ? (stages + want - 1) / want : 1, splits = stages > 0 ? (stages + per - 1) / per : 1;
@@ -1214,9 +1345,9 @@ LinearPlan linear_plan(int op, int64_t M, int64_t N, int64_t K)
             if (rest) c += rest <= kCus ? sh.stage1 : sh.stage2;
             c = c * (float)per + sh.fixed;
             if (splits > 1) c += kJoin + (float)splits * ((float)(M * N) * (8.0f / kPartialRate) + 0.15f);
-            if (cost == 0 || c < cost) {
+            if (c < cost) {
                 cost = c;
-                best = {t, splits, (int64_t)per * kStage, splits > 1 ? splits * M * N * 4 : 0};
+                best = {t, splits, (int64_t)per * kStage, {}, splits > 1 ? splits * M * N * 4 : 0};
             }
         }
     }
@@ -1228,6 +1359,7 @@ hipError_t launch_linear(const LinearParams &p0, int op, const LinearPlan &plan,
     LinearParams p = p0;
     p.splits = plan.splits;
     p.part = plan.part;
+    p.cut = plan.cut;
     if (plan.tile == kTileFew) return launch_few(p, s);
     if (p.splits > 1) p.f.finish = kFinPartial;
     hipError_t e;
