@@ -522,7 +522,7 @@ __device__ __forceinline__ uint32_t xcd_order(uint32_t b, uint32_t n)
 // and columns (l / 16) 4 + r.  With SwiGLU the wave's first C / 2
 // columns are gates, the others their ups.  WK waves hold sums of the same outputs:
 // they meet in LDS, where each finishes its share of the rows.
-template <int PITCH, int MI, int NJ>
+template <int PITCH, bool SPREAD, int MI, int NJ>
 __device__ __forceinline__ void put_rows(const floatx16 (&acc)[MI][NJ], int i, uint8_t *to)
 {
     const int lane = threadIdx.x & 63;
@@ -533,18 +533,35 @@ __device__ __forceinline__ void put_rows(const floatx16 (&acc)[MI][NJ], int i, u
             *(floatx4 *)(to + (lane & 31) * PITCH + (j * 32 + q * 8 + (lane >> 5) * 4) * 4) =
                 floatx4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
 }
-template <int PITCH, int MI, int NJ>
+template <int PITCH, bool SPREAD, int MI, int NJ>
 __device__ __forceinline__ void put_rows(const floatx4 (&acc)[MI][NJ], int i, uint8_t *to)
 {
     const int lane = threadIdx.x & 63;
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < 2; ++h) {
+        uint8_t *row = to + (h * 16 + (lane & 15)) * PITCH;
+        if constexpr (SPREAD) {
 #pragma unroll
-        for (int j = 0; j < NJ; ++j)
-            *(floatx4 *)(to + (h * 16 + (lane & 15)) * PITCH + (j * 16 + (lane >> 4) * 4) * 4) = acc[2 * i + h][j];
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int j = 0; j < NJ; j += 4) {
+                    floatx4 v;
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        float f;
+                        asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(f) : "a"(acc[2 * i + h][j + x][r]));
+                        v[x] = f;
+                    }
+                    *(floatx4 *)(row + (((lane >> 4) * 4 + r) * NJ + j) * 4) = v;
+                }
+        } else {
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) *(floatx4 *)(row + (j * 16 + (lane >> 4) * 4) * 4) = acc[2 * i + h][j];
+        }
+    }
 }
 
-template <int FIN, bool F32, int MI, int NJ, int WK, class Acc>
+template <int FIN, bool F32, int MI, int NJ, int WK, bool SPREAD_M, bool SPREAD_N, class Acc>
 __device__ __forceinline__ void finish_wave_as(const LinearParams &p, const Acc &acc, uint8_t *lds, int wk, int64_t m0,
                                                int64_t n0, float *partial, int64_t ldp)
 {
@@ -554,6 +571,10 @@ __device__ __forceinline__ void finish_wave_as(const LinearParams &p, const Acc 
     constexpr int ROWS = WK > 1 ? MI * 32 / WK : 32, ITS = (ROWS + RPI - 1) / RPI;
     const int lane = threadIdx.x & 63, g = lane % GROUPS, r0 = lane / GROUPS;
     const int64_t n = n0 + g * 8, ncols = GLU ? p.N >> 1 : p.N;
+    // from a place in the order of LDS's rows to the row of the product; a lane's first is its r0 or, spread, 8 r0
+    static_assert(!SPREAD_M || (RPI == 4 && MI == 4), "rows of a spread block");
+    const int first = SPREAD_M ? 8 * r0 : r0;
+    auto row_of = [&](int at) { return SPREAD_M ? (at & 15) * 8 + (at >> 5) * 2 + (at >> 4 & 1) : at; };
     auto get = [&](const uint8_t *src, float (&v)[8]) {
 #pragma unroll
         for (int w = 0; w < WK; ++w) {
@@ -592,7 +613,7 @@ __device__ __forceinline__ void finish_wave_as(const LinearParams &p, const Acc 
     auto all = [&](auto &&put_row) {
         if constexpr (WK > 1) {
 #pragma unroll
-            for (int i = 0; i < MI; ++i) put_rows<PITCH>(acc, i, lds + (wk * MI + i) * 32 * PITCH);
+            for (int i = 0; i < MI; ++i) put_rows<PITCH, SPREAD_N>(acc, i, lds + (wk * MI + i) * 32 * PITCH);
             __syncthreads();
             if (r0 < ROWS) share([&](auto P, int it, float (&v)[8], float (&u)[8]) { put_row(P, wk * ROWS + it * RPI, v, u); }, wk * ROWS);
         } else {
@@ -600,7 +621,7 @@ __device__ __forceinline__ void finish_wave_as(const LinearParams &p, const Acc 
             for (int i = 0; i < MI; ++i) {
                 unrolled<MI>([&](auto I) {
                     if (i == I.value) {
-                        put_rows<PITCH>(acc, I.value, lds);
+                        put_rows<PITCH, SPREAD_N>(acc, I.value, lds);
                         asm volatile("; rows %0" ::"i"(I.value) : "memory");   // the cases stay apart: registers have no index
                     }
                 });
@@ -614,19 +635,20 @@ __device__ __forceinline__ void finish_wave_as(const LinearParams &p, const Acc 
     if constexpr (FIN == kFinPartial) {
         const uint8_t *out = (const uint8_t *)partial;
         const uint32_t row_b = (uint32_t)ldp * 4, bytes = (uint32_t)max(min(p.M - m0, (int64_t)kWideRows), (int64_t)0) * row_b;
-        const uint32_t vo = n < ldp ? r0 * row_b + (uint32_t)n * 4 : kOOB;
-        all([&](auto, int row, float (&v)[8], float (&)[8]) {
+        const uint32_t vo = n < ldp ? first * row_b + (uint32_t)n * 4 : kOOB;
+        all([&](auto, int at, float (&v)[8], float (&)[8]) {
+            const int row = row_of(at);
             buf_store(uintx4{f32_bits(v[0]), f32_bits(v[1]), f32_bits(v[2]), f32_bits(v[3])}, out, bytes, vo, row * row_b);
             buf_store(uintx4{f32_bits(v[4]), f32_bits(v[5]), f32_bits(v[6]), f32_bits(v[7])}, out, bytes, vo, row * row_b + 16);
         });
     } else {
-        const FinishRows<FIN, F32> fin(p.f, m0, p.M, r0, n, n < ncols);
+        const FinishRows<FIN, F32> fin(p.f, m0, p.M, first, n, n < ncols);
         Extra x[2] = {};
         fin.fetch(x[0], WK > 1 ? wk * ROWS : 0);
-        all([&](auto P, int row, float (&v)[8], float (&u)[8]) {
+        all([&](auto P, int at, float (&v)[8], float (&u)[8]) {
             constexpr int I = decltype(P)::value;
-            if (ITS > 1) fin.fetch(x[1 - I], row + RPI);
-            fin.store(x[I], row, v, u);
+            if (ITS > 1) fin.fetch(x[1 - I], row_of(at + RPI));
+            fin.store(x[I], row_of(at), v, u);
         });
     }
 }
@@ -634,23 +656,24 @@ __device__ __forceinline__ void finish_wave_as(const LinearParams &p, const Acc 
 // OP: the operator, which says what there is to finish.  in_parts: the sums are those
 // of a part of the reduction, and go to `partial`, the wave's first row there, whose
 // rows are ldp apart, from column n0 on.
-template <int OP, int MI, int NJ, int WK, class Acc>
+template <int OP, int MI, int NJ, int WK, bool SPREAD_M = false, bool SPREAD_N = false, class Acc>
 __device__ __forceinline__ void finish_wave(const LinearParams &p, const Acc &acc, uint8_t *lds, int wk, int64_t m0,
                                             int64_t n0, bool in_parts, float *partial, int64_t ldp)
 {
     constexpr int PLAIN = OP == kLinDgrad ? kFinGrad : kFinFwd, GLU = OP == kLinDgrad ? kFinGradGlu : kFinFwdGlu;
     auto as = [&](auto F, auto F32) {
-        finish_wave_as<decltype(F)::value, decltype(F32)::value, MI, NJ, WK>(p, acc, lds, wk, m0, n0, partial, ldp);
+        finish_wave_as<decltype(F)::value, decltype(F32)::value, MI, NJ, WK, SPREAD_M, SPREAD_N>(p, acc, lds, wk, m0, n0, partial, ldp);
     };
-    if (in_parts) {
-        as(IC<kFinPartial>{}, IC<true>{});
-    } else if (OP != kLinWgrad && p.f.finish == GLU) {
+    if (in_parts) return as(IC<kFinPartial>{}, IC<true>{});
+    if constexpr (OP == kLinWgrad) {
+        as(IC<PLAIN>{}, IC<true>{});
+    } else if (p.f.finish == GLU) {
         if (OP == kLinFwd && p.f.f32) as(IC<GLU>{}, IC<OP == kLinFwd>{});
         else as(IC<GLU>{}, IC<false>{});
-    } else if (OP == kLinWgrad || (OP == kLinFwd && p.f.f32)) {
-        as(IC<PLAIN>{}, IC<OP != kLinDgrad>{});
+    } else if (OP == kLinFwd && p.f.f32) {
+        as(IC<PLAIN>{}, IC<OP == kLinFwd>{});
     } else {
-        as(IC<PLAIN>{}, IC<OP == kLinWgrad>{});
+        as(IC<PLAIN>{}, IC<false>{});
     }
 }
 
@@ -819,36 +842,45 @@ __global__ __launch_bounds__(64 * WM * WN * WK, 2) void linear_kernel(LinearPara
 // registers by then: it frees the stage's slots and hands out those of the next.
 constexpr int kWide = 256, kWideThreads = 256, kWideSlot = kWide * 128, kWideLds = 5 * kWideSlot;
 
-// Per-lane address in a stage of the wide tile of the fragment of a block of 16
-// rows / columns from `first`: lane l holds row / column l % 16 and reduction
-// values (l / 16) 8 on.
-template <bool ALONG>
-__device__ __forceinline__ uint32_t frag16_base(int first)
-{
-    const int lane = threadIdx.x & 63, r16 = lane & 15, q = lane >> 4;
-    if (ALONG) return (uint32_t)(first + r16) * 128 + (uint32_t)along(first + r16, q) * 16;
-    const int krow = q * 8 + (r16 >> 2), col = first + 4 * (r16 & 3);
-    return (uint32_t)krow * (kWide * 2) + (uint32_t)across<kWide / 8>(krow, col >> 3) * 16 + 8 * (r16 & 1);
-}
-
-// A wave's eight fragments of one operand at step KS (32 values) of a stage.
+// A wave's eight fragments of one operand at step KS (32 values) of a stage.  Along
+// the reduction fragment i holds 16 rows from 16 i on, lane l row l % 16 and
+// reduction values (l / 16) 8 on: a read each.  Across it a lane reads eight
+// neighbouring columns, from 8 (l % 16) on, at each of its eight reduction values,
+// and turns the 8 x 8 block itself, a v_perm_b32 a register: fragment i then holds
+// of lane l column 8 (l % 16) + i.  (The transposing LDS reads need no turning but
+// take LDS half as long again, which it has not got here: wgrad 2818 cycles a stage.)
 template <bool ALONG>
 struct WideFrags {
     uint32_t at;
-    __device__ __forceinline__ void init(uint32_t lds, int first) { at = lds + frag16_base<ALONG>(first); }
-    template <int KS, int I>
-    __device__ __forceinline__ bf16x8 read(uint32_t slot) const
+    __device__ __forceinline__ void init(uint32_t lds, int first)
     {
-        if constexpr (ALONG) {
-            return __builtin_bit_cast(bf16x8, ldsr_u128<I * 16 * 128>((at + slot) ^ (uint32_t)(KS << 6)));     // chunk q + 4 KS
-        } else {
-            constexpr int O = KS * 32 * 512;
-            const uint32_t x = (at + slot) ^ (uint32_t)(I << 5);       // the rows' swizzle moves whole blocks
-            const uintx2 lo = read_tr<O>(x), hi = read_tr<O + 4 * 512>(x);
-            return __builtin_bit_cast(bf16x8, uintx4{lo[0], lo[1], hi[0], hi[1]});
-        }
+        const int lane = threadIdx.x & 63, r16 = lane & 15, q = lane >> 4;
+        if (ALONG) at = lds + (uint32_t)(first + r16) * 128 + (uint32_t)along(first + r16, q) * 16;
+        else at = lds + (uint32_t)q * 8 * (kWide * 2) + (uint32_t)across<kWide / 8>(q * 8, first / 8 + r16) * 16;
+    }
+    template <int KS, int I>
+    __device__ __forceinline__ uintx4 read(uint32_t slot) const
+    {
+        if constexpr (ALONG) return ldsr_u128<I * 16 * 128>((at + slot) ^ (uint32_t)(KS << 6));     // chunk q + 4 KS
+        else return ldsr_u128<(KS * 32 + I) * kWide * 2>((at + slot) ^ (uint32_t)((I & 3) << 6));
+    }
+    // word W of fragment I
+    template <int I, int W>
+    static __device__ __forceinline__ uint32_t turned(const uintx4 (&raw)[8])
+    {
+        return __builtin_amdgcn_perm(raw[2 * W + 1][I / 2], raw[2 * W][I / 2], I & 1 ? 0x07060302u : 0x05040100u);
     }
 };
+
+// The LDS reads but the last N have arrived; what they brought passes through, so
+// that no use of it moves before.
+template <int N>
+__device__ __forceinline__ void wait_reads(uintx4 (&v)[8])
+{
+    asm volatile("s_waitcnt lgkmcnt(%0)" ::"i"(N) : "memory");
+#pragma unroll
+    for (int i = 0; i < 8; ++i) asm volatile("" : "+v"(v[i]));
+}
 
 template <bool ALA, bool ALB>
 __global__ __launch_bounds__(kWideThreads, 1) void linear_wide_kernel(LinearParams p, int tilesM, int tilesN)
@@ -900,37 +932,70 @@ __global__ __launch_bounds__(kWideThreads, 1) void linear_wide_kernel(LinearPara
     at.b.issue(smem_b, wave);
     at.a.issue(smem + kWideSlot, wave);
     at.b.issue(smem_b + kWideSlot, wave);
-    bf16x8 fa[2][8], fb[2][8];
+    uintx4 fa[2][8], fb[2][8];
+    // word W of fragment I out of what was read
+    auto turn = [&](auto ALONG, uintx4 (&f)[8], const uintx4 (&raw)[8], auto IW) {
+        constexpr int I = decltype(IW)::value / 4, W = decltype(IW)::value % 4;
+        if constexpr (!decltype(ALONG)::value) f[I][W] = WideFrags<false>::turned<I, W>(raw);
+        else if constexpr (W == 0) f[I] = raw[I];
+    };
+    using AlongA = IC<ALA>;
+    using AlongB = IC<ALB>;
     wait_vmcnt<2 * NL>();
     barrier();
-    unrolled<8>([&](auto I) { fa[0][I.value] = ra.template read<0, I.value>(0); });
-    unrolled<8>([&](auto I) { fb[0][I.value] = rb.template read<0, I.value>(0); });
-    wait_frags(fa[0], fb[0]);
+    {
+        uintx4 xa[8], xb[8];
+        unrolled<8>([&](auto I) { xa[I.value] = ra.template read<0, I.value>(0); });
+        unrolled<8>([&](auto I) { xb[I.value] = rb.template read<0, I.value>(0); });
+        wait_reads<0>(xa);
+        wait_reads<0>(xb);
+        unrolled<32>([&](auto IW) { turn(AlongA{}, fa[0], xa, IW); });
+        unrolled<32>([&](auto IW) { turn(AlongB{}, fb[0], xb, IW); });
+    }
 
     uint32_t a0 = 0, a1 = kWideSlot, a2 = 2 * kWideSlot, b0 = 0, b1 = kWideSlot;     // slots of this stage and the next ones
     auto step = [&](auto KC) {
         constexpr int KS = decltype(KC)::value, C = KS, NKS = 1 - KS;
         const uint32_t sa = KS ? a1 : a0, sb = KS ? b1 : b0;                         // where the next step's fragments are
         const uint32_t v = KS ? at.b.lane_offset() : at.a.lane_offset();
+        // reads every READ products: across the reduction the last of them turn what was read
+        constexpr int READ = ALA && ALB ? 3 : 2;
+        uintx4 xa[8], xb[8];
         unrolled<64>([&](auto X) {
             constexpr int x = decltype(X)::value, i = x >> 3, j = x & 7;
-            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[C][j], fa[C][i], acc[i][j], 0, 0, 0);
-            if constexpr (x % 3 == 0 && x < 48) {
-                // in the order in which the next step needs them
-                constexpr int y = x / 3;
-                if constexpr (y == 0) fa[1 - C][0] = ra.template read<NKS, 0>(sa);
-                else if constexpr (y <= 8) fb[1 - C][y - 1] = rb.template read<NKS, y - 1>(sb);
-                else fa[1 - C][y - 8] = ra.template read<NKS, y - 8>(sa);
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, fb[C][j]), __builtin_bit_cast(bf16x8, fa[C][i]),
+                                                                acc[i][j], 0, 0, 0);
+            if constexpr (x % READ == 0 && x < 16 * READ) {
+                constexpr int y = x / READ;
+                if constexpr (y < 8) xb[y] = rb.template read<NKS, y>(sb);
+                else xa[y - 8] = ra.template read<NKS, y - 8>(sa);
             }
             if constexpr (x % 8 == 4) {
                 if constexpr (KS == 0) at.a.issue_one(smem + a2, x / 8, v, wave);
                 else at.b.issue_one(smem_b + b0, x / 8, v, wave);
             }
+            if constexpr (!ALB) {
+                constexpr int T = ALA ? 1 : 2, FROM = ALA ? 32 : 32;
+                if constexpr (x == FROM) wait_reads<8>(xb);
+                if constexpr (x >= FROM && x < FROM + 32 / T)
+                    unrolled<T>([&](auto Y) { turn(AlongB{}, fb[1 - C], xb, IC<(x - FROM) * T + decltype(Y)::value>{}); });
+            }
+            if constexpr (!ALA) {
+                if constexpr (x == 48) wait_reads<0>(xa);
+                if constexpr (x >= 48) unrolled<2>([&](auto Y) { turn(AlongA{}, fa[1 - C], xa, IC<(x - 48) * 2 + decltype(Y)::value>{}); });
+            }
             if constexpr (x % 2 == 1) __builtin_amdgcn_sched_barrier(0);
         });
         if constexpr (KS == 0) at.a.advance();
         else at.b.advance();
-        wait_frags(fa[1 - C], fb[1 - C]);
+        if constexpr (ALA) {
+            wait_reads<0>(xa);
+            unrolled<8>([&](auto I) { fa[1 - C][I.value] = xa[I.value]; });
+        }
+        if constexpr (ALB) {
+            wait_reads<0>(xb);
+            unrolled<8>([&](auto I) { fb[1 - C][I.value] = xb[I.value]; });
+        }
         if constexpr (KS == 0) {
             wait_vmcnt<NL>();            // all but A of the stage after next has landed, for all waves after the barrier
             barrier();
@@ -948,8 +1013,11 @@ __global__ __launch_bounds__(kWideThreads, 1) void linear_wide_kernel(LinearPara
     }
     wait_vmcnt<0>();                     // zeros of stages past the end may still be landing in the ring
     barrier();
+    // across the reduction the epilogue reads the sums by instructions of its own, which wait for no product: 32 states
+    // after the loop's last one
+    if constexpr (!ALB) asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
     // a piece's sums go to a tile of their own, its columns in the waves' order
-    finish_wave<ALA ? ALB ? kLinFwd : kLinDgrad : kLinWgrad, 4, 4, 1>(p, acc, smem + wave * 32 * wave_pitch<128>(), 0, at.m0 + wm * 128,
+    finish_wave<ALA ? ALB ? kLinFwd : kLinDgrad : kLinWgrad, 4, 4, 1, !ALA, !ALB>(p, acc, smem + wave * 32 * wave_pitch<128>(), 0, at.m0 + wm * 128,
                                                                      slot < 0 ? at.col(wn) : wn * 128, slot >= 0,
                                                                      p.partials + ((int64_t)slot * kWide + wm * 128) * kWide, kWide);
 }
