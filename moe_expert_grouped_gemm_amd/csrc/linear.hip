@@ -6,17 +6,23 @@
 //   dgrad    C[m, k] = sum_n dy[m, n] w[n, k]     w across it
 //   wgrad    C[n, k] = sum_m dy[m, n] x[m, k]     both across it
 //
-// One kernel serves all three: a workgroup computes a TM x TN tile of C over
-// one part of the reduction, in stages of 64 values through a ring of LDS
-// slots filled by direct loads.  Operands keep in LDS the layout that they
-// have in memory: along the reduction as rows of 128 bytes read with
-// ds_read_b128, across it as 64 rows read with the transposing
-// ds_read_b64_tr_b16.  Products are v_mfma_f32_32x32x16_bf16 with the operands
-// swapped, so that a lane holds four neighbouring columns of one row and the
-// tile passes through LDS in 16-byte pieces, still in fp32: bias, activation
-// and residual are applied to unrounded sums and the result is rounded once.
-// Where the tiles alone do not fill the chip the reduction is cut in parts
-// whose fp32 sums a second kernel adds in order and finishes.
+// A workgroup computes a TM x TN tile of C over one part of the reduction, in
+// stages of 64 values through a ring of LDS slots filled by direct loads.
+// Operands keep in LDS the layout that they have in memory: along the reduction
+// as rows of 128 bytes, across it as 64 rows of the tile's columns, which lanes
+// read transposed (ds_read_b64_tr_b16) or, in the widest tile, turn themselves.
+// Products are bf16 matrix instructions with the operands swapped, so that a
+// lane holds four neighbouring columns of one row and the tile passes through
+// LDS in 16-byte pieces, still in fp32: bias, activation and residual are
+// applied to unrounded sums and the result is rounded once.  Where the tiles
+// alone do not fill the chip the reduction is cut in parts whose fp32 sums a
+// second kernel adds in order and finishes.
+//
+// What bounds them: products that fill the chip the matrix cores at the clock
+// that the power limit leaves them (8192^3: 1506 TFLOP/s at 1.5 to 1.8 GHz, 2.4
+// when idle); those of some hundred rows the loads into LDS, about 60 GB/s to a
+// CU, and the waits of a start and an end (1021 x 2880 x 2880: 24 us); those of
+// few rows memory (1 x 4096 x 4096: 3.5 TB/s, launch included).
 #include <utility>
 
 #include "dense.hpp"
@@ -273,7 +279,8 @@ __device__ __forceinline__ void buf_store(uintx4 v, const void *base, uint32_t b
 // Rows of a wave from row m0 on, each lane at its 8 columns.  Loads and stores
 // have no branch around them -- what is not there has a bound of 0 -- so that the
 // wait for a row's loads is a count that leaves the stores in flight (with a
-// branch it was for every store before: 1000 cycles a row).
+// branch it was for every store before: 1000 cycles a row, 38000 cycles a tile of
+// 256 x 256 with its copies unrolled, now 18600).
 template <int FIN, bool F32>
 struct FinishRows {
     static constexpr bool FWD = FIN == kFinFwd || FIN == kFinFwdGlu;
@@ -334,12 +341,13 @@ struct FinishRows {
 // Chunk swizzles of a stage in LDS.  Along the reduction (rows of 128 bytes):
 // the 16 lanes of a ds_read_b128 pass, reading one chunk of 16 consecutive
 // rows, cover all banks.  Across it (rows of CPR chunks): the four rows of a
-// transposing read's 16 lanes fall on different banks.
+// transposing read's 16 lanes fall on different banks; the widest tile's lanes read
+// 16 neighbouring chunks of a row and need none.
 __device__ __forceinline__ int along(int r, int c) { return c ^ ((r >> 1) & 7); }
 template <int CPR>
 __device__ __forceinline__ int across(int k, int c)
 {
-    return CPR >= 32 ? c ^ ((k & 3) << 2) ^ (((k >> 3) & 1) << 1) : CPR == 16 ? c ^ ((k & 3) << 2) : c ^ (((k >> 1) & 1) << 2);
+    return CPR >= 32 ? c : CPR == 16 ? c ^ ((k & 3) << 2) : c ^ (((k >> 1) & 1) << 2);
 }
 
 // One operand of a tile: R rows (ALONG) or columns (!ALONG) of a stage, loaded
@@ -363,7 +371,6 @@ struct Operand {
     int k;                                                 // ALONG: this lane's first reduction value
     int klen, k0;                                          // reduction values, and those before the stage
     uint32_t pitch, width;                                 // !ALONG: bytes of a row, and of its valid columns
-    uint32_t odd;                                          // !ALONG, long rows: voff of the odd loads, whose swizzle differs
 
     // rows0, rows1: valid rows from p0 and p1 (ALONG); pair: rows of base[0] from pair to pair; cols: valid columns (!ALONG)
     __device__ __forceinline__ void init(const uint16_t *p0, const uint16_t *p1, int rows0, int rows1, int pair, int64_t ld,
@@ -399,8 +406,6 @@ struct Operand {
             pitch = (uint32_t)ld * 2;
             width = (uint32_t)min(cols, (int64_t)R) * 2;
             voff = row * pitch + (uint32_t)min((int64_t)chunk * 8, cols - 8) * 2;
-            static_assert(CPR < 32 || RPL == 8, "a load is one octet of rows");
-            odd = CPR < 32 ? voff : row * pitch + (uint32_t)min((int64_t)across<CPR>(row + 8, t % CPR) * 8, cols - 8) * 2;
             step = kStage * ld * 2;
             k = 0;
             bound();
@@ -420,7 +425,6 @@ struct Operand {
     {
         constexpr int LPG = HALVES == 2 ? PAIR / RPL : NL;           // loads of a group
         const int q = i / LPG, h = HALVES == 2 ? q & 1 : 0;
-        if (!ALONG && CPR >= 32 && (i & 1)) v = odd;
         dma16(base[h], bytes[h], lds + wave * kWave * 16 + i * NT * 16, v, (HALVES == 2 ? (q >> 1) * pstep : 0u) + (i % LPG) * rstep);
     }
     __device__ __forceinline__ void advance()
@@ -519,7 +523,9 @@ __device__ __forceinline__ uint32_t xcd_order(uint32_t b, uint32_t n)
 // in fp32, so that lanes hold 8 neighbouring columns and a row leaves in whole
 // lines; nothing waits for another wave.  Lane l holds of a block of 32 x 32 row
 // l % 32 and columns (r / 4) 8 + (l / 32) 4 + r % 4, of one of 16 x 16 row l % 16
-// and columns (l / 16) 4 + r.  With SwiGLU the wave's first C / 2
+// and columns (l / 16) 4 + r.  Spread (the widest tile across the reduction), the
+// rows and columns of block i are every NJ-th from i on instead: NJ neighbouring
+// columns lie in one lane.  With SwiGLU the wave's first C / 2
 // columns are gates, the others their ups.  WK waves hold sums of the same outputs:
 // they meet in LDS, where each finishes its share of the rows.
 template <int PITCH, bool SPREAD, int MI, int NJ>
@@ -828,18 +834,22 @@ __global__ __launch_bounds__(64 * WM * WN * WK, 2) void linear_kernel(LinearPara
 // ------------------------------------------------------------------ wide tile
 // The tile for products that fill the chip: 256 x 256 by four waves of 128 x 128,
 // one on each SIMD, with 256 accumulators each.  A wave's share is square because
-// LDS is the narrow place: for a step of 16 reduction values the waves read 4 x 8
-// KB here, eight waves of 128 x 64 6 KB each, which with the 16 KB that the loads
-// bring in would take LDS as long as the products take the matrix cores.
+// LDS is the narrow place: the waves read 128 KB of a stage here, eight waves of
+// 128 x 64 would read 192 KB, which with the 64 KB that the loads bring in takes
+// LDS as long as the products take the matrix cores (8192^3: 1060 TFLOP/s so).
 //
-// One wave a SIMD hides nothing by itself, so the order of its instructions does:
-// a step's 16 products run while the next step's fragments are read and four loads
-// go out, each between two products (all 16 loads of a stage in one step held the
-// products up: 1259 TFLOP/s at 8192^3).  LDS holds three slots of A and two of B,
-// all of its 160 KB, so that the loads spread evenly over the four steps of stage t:
-//     B of t + 1, second half;  A of t + 2, first;  A of t + 2, second;  B of t + 2, first
-// The one barrier of a stage comes before its last step, whose operands are in
-// registers by then: it frees the stage's slots and hands out those of the next.
+// One wave a SIMD hides nothing by itself, so the order of its instructions does.
+// A stage is two steps of 32 reduction values, 64 products of 16 x 16 x 32 each.
+// While a step's run, the next one's fragments are read, one read every second or
+// third product, and eight loads go out, one every eighth: in one go either holds
+// the products up (3169 cycles a stage, spread 2371, the products alone 2048).
+// 16 x 16 x 32 because at the power limit it gets the same work done in 1.32 us a
+// stage that 32 x 32 x 16 does in 1.41.
+//
+// LDS holds three slots of A and two of B, all of its 160 KB.  Step 0 of stage t
+// loads A of t + 2, step 1 B of t + 2 into the slot that B of t has left.  The one
+// barrier of a stage stands between its steps: stage t's fragments are all in
+// registers by then, and all loads but those of A of t + 2 have landed.
 constexpr int kWide = 256, kWideThreads = 256, kWideSlot = kWide * 128, kWideLds = 5 * kWideSlot;
 
 // A wave's eight fragments of one operand at step KS (32 values) of a stage.  Along
@@ -856,13 +866,13 @@ struct WideFrags {
     {
         const int lane = threadIdx.x & 63, r16 = lane & 15, q = lane >> 4;
         if (ALONG) at = lds + (uint32_t)(first + r16) * 128 + (uint32_t)along(first + r16, q) * 16;
-        else at = lds + (uint32_t)q * 8 * (kWide * 2) + (uint32_t)across<kWide / 8>(q * 8, first / 8 + r16) * 16;
+        else at = lds + (uint32_t)(q * 8 * kWide + first + r16 * 8) * 2;
     }
     template <int KS, int I>
     __device__ __forceinline__ uintx4 read(uint32_t slot) const
     {
         if constexpr (ALONG) return ldsr_u128<I * 16 * 128>((at + slot) ^ (uint32_t)(KS << 6));     // chunk q + 4 KS
-        else return ldsr_u128<(KS * 32 + I) * kWide * 2>((at + slot) ^ (uint32_t)((I & 3) << 6));
+        else return ldsr_u128<(KS * 32 + I) * kWide * 2>(at + slot);
     }
     // word W of fragment I
     template <int I, int W>
