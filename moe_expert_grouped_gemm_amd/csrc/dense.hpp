@@ -45,6 +45,18 @@ struct WideCut {
     __host__ __device__ int pieces() const { return parts * rest + tails + (rest - tails) * cuts; }
 };
 
+// dbias[n] (+)= sum over rows of dy[r, n].  parts > 1: sums of each part's rows in
+// partials, [parts][N], joined afterwards.
+struct ColsumParams {
+    const uint16_t *dy;       // [M, N] bf16
+    float *dbias;             // or null: not wanted
+    float *partials;
+    int64_t M, N;
+    int parts;
+    int accumulate;
+};
+int colsum_parts(int64_t M, int64_t N);
+
 // C[m, n] = sum over q < K of A(m, q) B(n, q): forward A = x, B = w; dgrad
 // A = dy, B = w by columns; wgrad A = dy and B = x by columns.
 struct LinearParams {
@@ -55,6 +67,8 @@ struct LinearParams {
     int64_t part;             // reduction values a part (a multiple of 64)
     float *partials;          // workspace: splits x [M, N] fp32, where splits > 1; or the cut's pieces, a tile each
     WideCut cut;              // of the widest tile
+    ColsumParams sums;        // wgrad: the bias's gradient
+    int join_blocks;          // workgroups of the join that add the product's parts; the others join the column sums
     FinishParams f;
 };
 
@@ -69,10 +83,6 @@ struct LinearPlan {
 LinearPlan linear_plan(int op, int64_t M, int64_t N, int64_t K);
 hipError_t launch_linear(const LinearParams &p, int op, const LinearPlan &plan, hipStream_t s);
 
-// dbias[n] (+)= sum over rows of dy[r, n]; parts > 1: partial sums [parts][N].
-int colsum_parts(int64_t M, int64_t N);
-hipError_t launch_colsum(const uint16_t *dy, float *dbias, float *partials, int64_t M, int64_t N, int accumulate,
-                         hipStream_t s);
 // dc = dout * act'(c) over [M, N] (SwiGLU: dout [M, N/2]).
 hipError_t launch_act_bwd(const uint16_t *dout, const uint16_t *c, uint16_t *dc, int64_t M, int64_t N, int act,
                           float limit, hipStream_t s);

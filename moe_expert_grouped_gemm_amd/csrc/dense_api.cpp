@@ -177,11 +177,14 @@ int pt_linear_wgrad(const void *x, const void *dy, float *main_grad, float *dbia
     p.f.finish = kFinFwd;
     p.f.act = kActNone;
     p.f.f32 = 1;
-    hipError_t e = launch_linear(p, kLinWgrad, plan, (hipStream_t)stream);
-    if (e == hipSuccess && dbias)
-        e = launch_colsum((const uint16_t *)dy, dbias, (float *)((uint8_t *)workspace + at), M, N, accumulate,
-                          (hipStream_t)stream);
-    return hip_status(e);
+    p.sums.dy = (const uint16_t *)dy;
+    p.sums.dbias = dbias;
+    p.sums.partials = (float *)((uint8_t *)workspace + at);
+    p.sums.M = M;
+    p.sums.N = N;
+    p.sums.parts = colsum_parts(M, N);
+    p.sums.accumulate = accumulate;
+    return hip_status(launch_linear(p, kLinWgrad, plan, (hipStream_t)stream));
 }
 
 int pt_linear_act_bwd(const void *dout, const void *c, void *dc, int64_t M, int64_t N, int act, float swiglu_limit,

@@ -1032,6 +1032,18 @@ __global__ __launch_bounds__(kWideThreads, 1) void linear_wide_kernel(LinearPara
                                                                      p.partials + ((int64_t)slot * kWide + wm * 128) * kWide, kWide);
 }
 
+// The parts' column sums added in order, a column to a thread.  Where a product's
+// parts are joined too, the same launch does both.
+__device__ __forceinline__ void colsum_join(const ColsumParams &p, int block)
+{
+    const int64_t c = (int64_t)block * kThreads + threadIdx.x;
+    if (c >= p.N) return;
+    float sum = 0.0f;
+#pragma unroll 8
+    for (int i = 0; i < p.parts; ++i) sum += p.partials[(int64_t)i * p.N + c];
+    p.dbias[c] = p.accumulate ? p.dbias[c] + sum : sum;
+}
+
 // The pieces of a cut tile added in their order along the reduction, then what the
 // tile itself would have done.  A workgroup takes 8 rows (SwiGLU: 16), a thread 8 columns.
 template <int FIN>
@@ -1039,6 +1051,7 @@ __global__ __launch_bounds__(kThreads) void linear_wide_join_kernel(LinearParams
 {
     constexpr bool GLU = FIN == kFinFwdGlu;
     constexpr int GROUPS = kWide / (GLU ? 16 : 8), ROWS = kThreads / GROUPS;
+    if (FIN == kFinFwd && (int)blockIdx.x >= p.join_blocks) return colsum_join(p.sums, (int)blockIdx.x - p.join_blocks);
     const WideCut &cut = p.cut;
     const int t = blockIdx.x / (kWide / ROWS), g = threadIdx.x % GROUPS;
     const int row = blockIdx.x % (kWide / ROWS) * ROWS + (int)threadIdx.x / GROUPS;
@@ -1185,8 +1198,9 @@ template <int FIN>
 __global__ __launch_bounds__(kThreads) void linear_join_kernel(LinearParams p)
 {
     constexpr bool GLU = FIN == kFinFwdGlu;
+    if (FIN == kFinFwd && (int)blockIdx.x >= p.join_blocks) return colsum_join(p.sums, (int)blockIdx.x - p.join_blocks);
     const int64_t half = p.N >> 1, groups = (GLU ? half : p.N) / 8, total = p.M * groups;
-    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kThreads) {
+    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total; i += (int64_t)p.join_blocks * kThreads) {
         const int64_t m = i / groups, n = (i - m * groups) * 8;
         float v[8] = {}, u[8] = {};
 #pragma unroll 8
@@ -1210,9 +1224,9 @@ __global__ __launch_bounds__(kThreads) void linear_join_kernel(LinearParams p)
 // A workgroup adds 64 columns over one part of the rows: 8 lanes of 8 columns,
 // 32 rows side by side, joined in LDS in their order.
 constexpr int kColsumCols = 64, kColsumRows = 32;
-__global__ __launch_bounds__(kThreads) void colsum_kernel(const uint16_t *__restrict__ dy, float *dbias, float *partials,
-                                                          int64_t M, int64_t N, int accumulate)
+__global__ __launch_bounds__(kThreads) void colsum_kernel(ColsumParams p)
 {
+    const int64_t M = p.M, N = p.N;
     __shared__ float s[kColsumRows][kColsumCols + 4];
     const int lane = threadIdx.x & 7, side = threadIdx.x >> 3;
     const int64_t n = (int64_t)blockIdx.x * kColsumCols + lane * 8;
@@ -1221,7 +1235,7 @@ __global__ __launch_bounds__(kThreads) void colsum_kernel(const uint16_t *__rest
 #pragma unroll 4
         for (int64_t r = (int64_t)blockIdx.y * kColsumRows + side; r < M; r += (int64_t)gridDim.y * kColsumRows) {
             float f[8];
-            unpack8(*(const uintx4 *)(dy + r * N + n), f);
+            unpack8(*(const uintx4 *)(p.dy + r * N + n), f);
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] += f[j];
         }
@@ -1234,20 +1248,11 @@ __global__ __launch_bounds__(kThreads) void colsum_kernel(const uint16_t *__rest
     float sum = 0.0f;
 #pragma unroll
     for (int r = 0; r < kColsumRows; ++r) sum += s[r][threadIdx.x];
-    if (gridDim.y > 1) partials[(int64_t)blockIdx.y * N + c] = sum;
-    else dbias[c] = accumulate ? dbias[c] + sum : sum;
+    if (p.parts > 1) p.partials[(int64_t)blockIdx.y * N + c] = sum;
+    else p.dbias[c] = p.accumulate ? p.dbias[c] + sum : sum;
 }
 
-__global__ __launch_bounds__(kThreads) void colsum_join_kernel(const float *__restrict__ partials, float *dbias, int parts,
-                                                               int64_t N, int accumulate)
-{
-    const int64_t c = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (c >= N) return;
-    float sum = 0.0f;
-#pragma unroll 8
-    for (int i = 0; i < parts; ++i) sum += partials[(int64_t)i * N + c];
-    dbias[c] = accumulate ? dbias[c] + sum : sum;
-}
+__global__ __launch_bounds__(kThreads) void colsum_join_kernel(ColsumParams p) { colsum_join(p, blockIdx.x); }
 
 template <int FIN>
 __global__ __launch_bounds__(kThreads) void act_bwd_kernel(const uint16_t *dout, FinishParams f, int64_t M)
@@ -1286,6 +1291,12 @@ constexpr TileShape kTiles[] = {{64, 16, 1, 0, 0, 0},
 constexpr int kCus = 256;
 constexpr float kJoin = 3.2f, kPartialRate = 5e6f;      // us of the join's launch; bytes a us of partial sums
 
+// Workgroups that join the parts of the column sums.
+int sums_join_blocks(const LinearParams &p)
+{
+    return p.sums.dbias && p.sums.parts > 1 ? (int)((p.sums.N + kThreads - 1) / kThreads) : 0;
+}
+
 template <bool ALA, bool ALB, int TM, int TN, int WM, int WN, int WK, int NS>
 hipError_t launch_tile(const LinearParams &p, hipStream_t s)
 {
@@ -1312,12 +1323,22 @@ hipError_t launch_wide(const LinearParams &p, hipStream_t s)
     const int64_t cols = glu ? p.N / 2 : p.N, tn = glu ? kWide / 2 : kWide;
     const int tilesM = (int)((p.M + kWide - 1) / kWide), tilesN = (int)((cols + tn - 1) / tn);
     hipLaunchKernelGGL(kern, dim3((unsigned)(p.cut.whole + p.cut.pieces())), dim3(kWideThreads), kWideLds, s, p, tilesM, tilesN);
-    if (p.cut.rest) {
-        const dim3 g((unsigned)p.cut.rest * (glu ? 16 : 32)), b(kThreads);
-        constexpr int PLAIN = ALA && !ALB ? kFinGrad : kFinFwd, GLU = ALA && !ALB ? kFinGradGlu : kFinFwdGlu;
-        if (p.f.finish == GLU) hipLaunchKernelGGL(linear_wide_join_kernel<GLU>, g, b, 0, s, p, tilesM, tilesN);
-        else hipLaunchKernelGGL(linear_wide_join_kernel<PLAIN>, g, b, 0, s, p, tilesM, tilesN);
-    }
+    return hipGetLastError();
+}
+
+// The product's parts joined, and the column sums' along with them.
+template <int FIN>
+hipError_t launch_join(LinearParams p, bool wide, hipStream_t s)
+{
+    constexpr bool GLU = FIN == kFinFwdGlu;
+    const int64_t cols = GLU ? p.N / 2 : p.N, tn = GLU ? kWide / 2 : kWide;
+    const int64_t grid = wide ? p.cut.rest * (GLU ? 16 : 32) : (p.M * (cols / 8) + kThreads - 1) / kThreads;
+    p.join_blocks = (int)(!wide && grid > 16384 ? 16384 : grid);
+    const dim3 g((unsigned)(p.join_blocks + sums_join_blocks(p))), b(kThreads);
+    if (wide)
+        hipLaunchKernelGGL(linear_wide_join_kernel<FIN>, g, b, 0, s, p, (int)((p.M + kWide - 1) / kWide), (int)((cols + tn - 1) / tn));
+    else
+        hipLaunchKernelGGL(linear_join_kernel<FIN>, g, b, 0, s, p);
     return hipGetLastError();
 }
 
@@ -1445,18 +1466,25 @@ hipError_t launch_linear(const LinearParams &p0, int op, const LinearPlan &plan,
     else if (op == kLinFwd) e = launch_op<true, true>(p, plan.tile, s);
     else if (op == kLinDgrad) e = launch_op<true, false>(p, plan.tile, s);
     else e = launch_op<false, false>(p, plan.tile, s);
-    if (e != hipSuccess || p.splits == 1) return e;
-    p.f.finish = p0.f.finish;
-    const int64_t items = p.M * ((p.f.finish == kFinFwdGlu ? p.N / 2 : p.N) / 8);
-    const int64_t grid = (items + kThreads - 1) / kThreads;
-    const dim3 g((unsigned)(grid > 16384 ? 16384 : grid)), b(kThreads);
-    switch (p.f.finish) {
-    case kFinFwd: hipLaunchKernelGGL(linear_join_kernel<kFinFwd>, g, b, 0, s, p); break;
-    case kFinFwdGlu: hipLaunchKernelGGL(linear_join_kernel<kFinFwdGlu>, g, b, 0, s, p); break;
-    case kFinGrad: hipLaunchKernelGGL(linear_join_kernel<kFinGrad>, g, b, 0, s, p); break;
-    default: hipLaunchKernelGGL(linear_join_kernel<kFinGradGlu>, g, b, 0, s, p); break;
+    if (e != hipSuccess) return e;
+    const bool wide = plan.tile == kTile256, join = wide ? p.cut.rest > 0 : p.splits > 1;
+    if (p.sums.dbias) {
+        // after the product, which leaves dy in the caches
+        hipLaunchKernelGGL(colsum_kernel, dim3((unsigned)((p.sums.N + kColsumCols - 1) / kColsumCols), p.sums.parts), dim3(kThreads), 0,
+                           s, p.sums);
+        if (p.sums.parts > 1 && !join)
+            hipLaunchKernelGGL(colsum_join_kernel, dim3((unsigned)sums_join_blocks(p)), dim3(kThreads), 0, s, p.sums);
+        e = hipGetLastError();
+        if (e != hipSuccess) return e;
     }
-    return hipGetLastError();
+    if (!join) return hipSuccess;
+    p.f.finish = p0.f.finish;
+    switch (p.f.finish) {
+    case kFinFwd: return launch_join<kFinFwd>(p, wide, s);
+    case kFinFwdGlu: return launch_join<kFinFwdGlu>(p, wide, s);
+    case kFinGrad: return launch_join<kFinGrad>(p, wide, s);
+    default: return launch_join<kFinGradGlu>(p, wide, s);
+    }
 }
 
 int colsum_parts(int64_t M, int64_t N)
@@ -1466,18 +1494,6 @@ int colsum_parts(int64_t M, int64_t N)
     const int64_t most = (1024 + cols - 1) / cols;
     if (parts > most) parts = most;
     return (int)(parts < 1 ? 1 : parts);
-}
-
-hipError_t launch_colsum(const uint16_t *dy, float *dbias, float *partials, int64_t M, int64_t N, int accumulate,
-                         hipStream_t s)
-{
-    const int parts = colsum_parts(M, N);
-    hipLaunchKernelGGL(colsum_kernel, dim3((unsigned)((N + kColsumCols - 1) / kColsumCols), parts), dim3(kThreads), 0, s, dy,
-                       dbias, partials, M, N, accumulate);
-    if (parts > 1)
-        hipLaunchKernelGGL(colsum_join_kernel, dim3((unsigned)((N + kThreads - 1) / kThreads)), dim3(kThreads), 0, s,
-                           partials, dbias, parts, N, accumulate);
-    return hipGetLastError();
 }
 
 hipError_t launch_act_bwd(const uint16_t *dout, const uint16_t *c, uint16_t *dc, int64_t M, int64_t N, int act,
