@@ -942,6 +942,24 @@ __global__ __launch_bounds__(kWideThreads, 1) void linear_wide_kernel(LinearPara
     at.b.issue(smem_b, wave);
     at.a.issue(smem + kWideSlot, wave);
     at.b.issue(smem_b + kWideSlot, wave);
+    if (at.m0 + wm * 128 >= p.M || at.col(wn) >= (at.glu ? p.N >> 1 : p.N)) {
+        // nothing of this wave's share is in the matrix: it loads, and keeps the others' barriers (2880 columns are 11.25
+        // tiles: the power that its products would take lets the clock rise, 251 to 244 us for 16384 x 2880 x 2880 wgrad)
+        wait_vmcnt<2 * NL>();
+        barrier();
+        int sa = 2 * kWideSlot, sb = 0;
+        for (int kt = 0; kt < nk; ++kt) {
+            at.a.issue(smem + sa, wave);
+            wait_vmcnt<NL>();
+            barrier();
+            at.b.issue(smem_b + sb, wave);
+            sa = sa == 2 * kWideSlot ? 0 : sa + kWideSlot;
+            sb = kWideSlot - sb;
+        }
+        wait_vmcnt<0>();
+        barrier();
+        return;
+    }
     uintx4 fa[2][8], fb[2][8];
     // word W of fragment I out of what was read
     auto turn = [&](auto ALONG, uintx4 (&f)[8], const uintx4 (&raw)[8], auto IW) {
@@ -1371,10 +1389,12 @@ hipError_t launch_few(const LinearParams &p, hipStream_t s)
 // take the tiles' tails, f of them one after another, and then what is left of the
 // tails in pieces: a tail is as long as lets both kinds of CUs end together.  Pieces
 // of a kind start at the same places of the reduction, so that an XCD's L2 serves
-// its tiles' common rows once.
+// its tiles' common rows once.  No part or piece is shorter than its start and end
+// (16384 x 2880 x 2880 wgrad: 260 us, three equal parts 286; 8192 x 2880 x 11520: 401,
+// whole tiles 445).
 WideCut wide_cut(int tiles, int stages)
 {
-    constexpr float kPiece = 8.0f;                       // stages that a piece costs besides its own
+    constexpr float kPiece = 8.0f;                       // a piece's start and end, in stages (23000 cycles)
     WideCut cut = {tiles, 0, 0, 0, 0, 0, 0};
     const int r = tiles % kCus;
     if (r == 0) return cut;
