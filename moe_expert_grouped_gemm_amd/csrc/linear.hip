@@ -1389,9 +1389,9 @@ hipError_t launch_few(const LinearParams &p, hipStream_t s)
 // take the tiles' tails, f of them one after another, and then what is left of the
 // tails in pieces: a tail is as long as lets both kinds of CUs end together.  Pieces
 // of a kind start at the same places of the reduction, so that an XCD's L2 serves
-// its tiles' common rows once.  No part or piece is shorter than its start and end
-// (16384 x 2880 x 2880 wgrad: 260 us, three equal parts 286; 8192 x 2880 x 11520: 401,
-// whole tiles 445).
+// its tiles' common rows once.  Parts and pieces are at least about as long as their
+// start and end (16384 x 2880 x 2880 wgrad: 260 us, three equal parts 286; 8192 x
+// 2880 x 11520: 401, whole tiles 445).
 WideCut wide_cut(int tiles, int stages)
 {
     constexpr float kPiece = 8.0f;                       // a piece's start and end, in stages (23000 cycles)
