@@ -5,8 +5,8 @@ training step with its backward, and decoding.
     python examples/moe_block.py            # 4096 tokens of 1024, 32 experts of inner size 512, 4 each, a shared one of 1024
 
 Every product, norm, choice and join of rows is the package's; torch holds the
-memory, adds up the experts' row counts, and projects the router where the
-experts are no multiple of 8.
+memory, adds up the experts' row counts, lays the router's gradient out, and
+projects the router where the experts are no multiple of 8.
 """
 import os
 import sys
@@ -73,6 +73,17 @@ class MoeBlock:
         pt.pt_linear_wgrad(x, dy, grad, None, M, N, K, 1,
                            workspace=self._new(pt.pt_linear_workspace_size(pt.PT_OP_WGRAD, M, N, K), torch.uint8))
 
+    def _in_parts(self, x):
+        """fp32 [T, n] for the products, which take bf16: three parts beside each other whose sum is x to its last bit (8 bits
+        each), then zeros up to a multiple of 8 columns."""
+        T, n = x.shape
+        parts = self._new((T, -(-3 * n // 8) * 8))
+        parts[:, 3 * n :] = 0
+        for i in range(3):
+            part = parts[:, i * n : (i + 1) * n].copy_(x)
+            x = x - part.float()
+        return parts
+
     def _norm(self, x, residual, rstd=None):
         stream, y = self._new(x.shape), self._new(x.shape)
         pt.pt_rmsnorm_fwd(x, residual, self.norm, stream, y, None, None, rstd, x.shape[0], self.H, EPS)
@@ -138,18 +149,18 @@ class MoeBlock:
         pt.pt_moe_combine(da, None, row_of, None, dy, T, M, H, k)
         dlogits = torch.empty_like(logits)
         pt.pt_moe_route_bwd(logits, ids, dweights, dlogits, T, E, k, pt.PT_FP32, pt.PT_GATE_SOFTMAX, 1)
-        if E % 8:
-            self.grad["router"] += dlogits.t() @ y.float()
-            dy = (dy.float() + dlogits @ self.router.float()).bfloat16()
-        else:
-            dlogits = dlogits.bfloat16()
-            self._linear_wgrad(y, dlogits, self.grad["router"])
-            self._linear_dgrad(dlogits, self.router, dy, add=dy)
+        d = self._in_parts(dlogits)
+        dw = torch.zeros((d.shape[1], H), device=self.device)
+        self._linear_wgrad(y, d, dw)
+        self.grad["router"] += dw[2 * E : 3 * E] + dw[E : 2 * E] + dw[:E]
+        w = [self.router] * 3 + [self.router.new_zeros(d.shape[1] - 3 * E, H)]
         if self.S:
             dsc = self._linear_dgrad(dout, self.s2, self._new((T, 2 * self.S)), sc, act=pt.PT_ACT_SWIGLU)
             self._linear_wgrad(sh, dout, self.grad["s2"])
             self._linear_wgrad(y, dsc, self.grad["s1"])
-            self._linear_dgrad(dsc, self.s1, dy, add=dy)
+            d, w = torch.cat((d, dsc), 1), w + [self.s1]
+        # through router and shared expert in one product, onto the experts' sum: dy is rounded there and here
+        self._linear_dgrad(d, torch.cat(w), dy, add=dy)
         ds = self._new((T, H))
         pt.pt_rmsnorm_bwd(dy, stream, self.norm, rstd, dstream, ds, self.grad["norm"], T, H, pt.PT_BF16, 1,
                           workspace=self._new(pt.pt_rmsnorm_workspace_size(T, H), torch.uint8))
