@@ -94,9 +94,9 @@ class MoeBlock:
             return (y @ self.router.t()).float()
         return self._linear(y, self.router, self._new((y.shape[0], self.E), torch.float32))
 
-    def _shared(self, y, residual=None):
-        """The shared expert's output, and what its backward needs."""
-        c, h = self._new((y.shape[0], 2 * self.S)), self._new((y.shape[0], self.S))
+    def _shared(self, y, residual=None, save=True):
+        """The shared expert's output, and what its backward needs (save: the sums before SwiGLU too)."""
+        c, h = self._new((y.shape[0], 2 * self.S)) if save else None, self._new((y.shape[0], self.S))
         self._linear(y, self.s1, h, c, act=pt.PT_ACT_SWIGLU)
         return self._linear(h, self.s2, self._new(y.shape), residual=residual), c, h
 
@@ -198,7 +198,7 @@ class MoeBlock:
                              T, self.E, self.H, self.I, self.k, pt.PT_FP32, pt.PT_GATE_SOFTMAX, 1, 1.0, pt.PT_BF16,
                              workspace=self._new(n, torch.uint8))
         if self.S:
-            out, _, _ = self._shared(y, residual=out)
+            out, _, _ = self._shared(y, residual=out, save=False)
         return out, stream
 
 

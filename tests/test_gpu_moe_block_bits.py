@@ -58,3 +58,18 @@ def test_the_routers_and_the_norms_gradients(dev, example, monkeypatch, T, H, I,
     off = UNIT * experts.abs() + ((2 * S + 3 * E) / 16 + 64 + k) * 2.0 ** -23 * 1.01 * size
     off = off + UNIT * (want.abs() + off)
     assert ((seen["dy"].to(F64) - want).abs() <= off).all()
+
+
+def test_decoding_keeps_nothing_for_a_backward(dev, example, monkeypatch):  # noqa: F811
+    """The same bits as the forward's shared expert, without its sums being stored."""
+    T, H, I, E, k, S = 7, 128, 96, 8, 2, 64
+    block, (x, residual, _, _) = make(example, dev, T, H, I, E, k, S)
+    few, _ = block.decode(x, residual)
+    kept = []
+    watch(monkeypatch, ptm, "pt_linear_fwd", lambda a, kw: kept.append(a[5]))
+    again, _ = block.decode(x, residual)
+    torch.cuda.synchronize()
+    assert torch.equal(few, again)
+    assert len(kept) == 3 and all(c is None for c in kept)
+    block.forward(x, residual)
+    assert any(c is not None for c in kept[3:])
