@@ -31,7 +31,10 @@ constexpr int64_t kBlockStreamBytes = (int64_t)80 << 20;
 __host__ __device__ constexpr int team_threads(int W) { return W > 1 ? 64 * W : kThreads; }
 
 // The gate's bf16 values of row r (element base of the matrix), or null where it
-// is one number a row.  Chosen once per row: one address for both layouts.
+// is one number a row.  One address for both layouts, chosen once per row and before
+// the loop over the row's columns: with a load for each layout inside the loop the
+// compiler joined the two into one that took the whole matrix's address for a gate
+// per column as well, far past the vector's end.
 __device__ __forceinline__ const uint16_t *gate_row(const void *gate, int kind, int64_t base)
 {
     return kind == kGateCols || kind == kGateFull ? (const uint16_t *)gate + (kind == kGateFull ? base : 0) : nullptr;

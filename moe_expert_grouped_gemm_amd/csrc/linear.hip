@@ -20,9 +20,10 @@
 //
 // What bounds them: products that fill the chip the matrix cores at the clock
 // that the power limit leaves them (8192^3: 1506 TFLOP/s at 1.5 to 1.8 GHz, 2.4
-// when idle); those of some hundred rows the loads into LDS, about 60 GB/s to a
-// CU, and the waits of a start and an end (1021 x 2880 x 2880: 24 us); those of
-// few rows memory (1 x 4096 x 4096: 3.5 TB/s, launch included).
+// when idle); those of some hundred rows the loads into LDS, about 84 GB/s to a
+// CU while its stages run, which is near the most that direct loads bring in, and
+// the waits of a start and an end (1021 x 2880 x 2880: 24 us, 7 of them start and
+// end); those of few rows memory (1 x 4096 x 4096: 3.5 TB/s, launch included).
 #include <utility>
 
 #include "dense.hpp"
@@ -1003,7 +1004,7 @@ __global__ __launch_bounds__(kWideThreads, 1) void linear_wide_kernel(LinearPara
                 else at.b.issue_one(smem_b + b0, x / 8, v, wave);
             }
             if constexpr (!ALB) {
-                constexpr int T = ALA ? 1 : 2, FROM = ALA ? 32 : 32;
+                constexpr int T = ALA ? 1 : 2, FROM = 32;
                 if constexpr (x == FROM) wait_reads<8>(xb);
                 if constexpr (x >= FROM && x < FROM + 32 / T)
                     unrolled<T>([&](auto Y) { turn(AlongB{}, fb[1 - C], xb, IC<(x - FROM) * T + decltype(Y)::value>{}); });
@@ -1115,9 +1116,9 @@ constexpr int kFewWaves = 8, kFewCols = 16;
 
 __global__ __launch_bounds__(kFewWaves * kWave) void linear_few_kernel(LinearParams p)
 {
-    constexpr int MT = 1, U = 4;                             // steps of a batch; two batches are in flight
+    constexpr int U = 4;                                     // steps of a batch; two batches are in flight
     constexpr int PITCH = kFewCols + 4;
-    __shared__ __attribute__((aligned(16))) float red[kFewWaves][MT * 16][PITCH];
+    __shared__ __attribute__((aligned(16))) float red[kFewWaves][16][PITCH];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r16 = lane & 15, q = lane >> 4;
     const bool glu = p.f.finish == kFinFwdGlu;
@@ -1126,15 +1127,11 @@ __global__ __launch_bounds__(kFewWaves * kWave) void linear_few_kernel(LinearPar
     int64_t n = glu && r16 >= 8 ? half + n0 + r16 - 8 : n0 + r16;
     if (n >= p.N) n = p.N - 1;                               // read, never stored
     const uint16_t *w = p.b + n * p.ldb + q * 16;
-    const uint16_t *x[MT];
-#pragma unroll
-    for (int i = 0; i < MT; ++i) x[i] = p.a + min((int64_t)i * 16 + r16, p.M - 1) * p.lda + q * 16;
-    floatx4 acc[MT];
-#pragma unroll
-    for (int i = 0; i < MT; ++i) acc[i] = floatx4{0, 0, 0, 0};
+    const uint16_t *x = p.a + min((int64_t)r16, p.M - 1) * p.lda + q * 16;
+    floatx4 acc = {0, 0, 0, 0};
 
     struct Batch {
-        uintx4 w[U][2], x[U][MT][2];
+        uintx4 w[U][2], x[U][2];
     };
     const int K = (int)p.K, full = K / 64;
     auto load = [&](Batch &b, int s0) {
@@ -1145,23 +1142,19 @@ __global__ __launch_bounds__(kFewWaves * kWave) void linear_few_kernel(LinearPar
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 b.w[u][h] = *(const uintx4 *)(w + s + h * 8);
-#pragma unroll
-                for (int i = 0; i < MT; ++i) b.x[u][i][h] = *(const uintx4 *)(x[i] + s + h * 8);
+                b.x[u][h] = *(const uintx4 *)(x + s + h * 8);
             }
         }
     };
-    auto mma = [&](const uintx4 &wv, const uintx4 &xv, int i) {
-        acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, wv), __builtin_bit_cast(bf16x8, xv),
-                                                         acc[i], 0, 0, 0);
+    auto mma = [&](const uintx4 &wv, const uintx4 &xv) {
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, wv), __builtin_bit_cast(bf16x8, xv), acc, 0, 0, 0);
     };
     auto use = [&](const Batch &b, int s0) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (s0 + u * kFewWaves >= full) break;
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int i = 0; i < MT; ++i) mma(b.w[u][h], b.x[u][i][h], i);
+            for (int h = 0; h < 2; ++h) mma(b.w[u][h], b.x[u][h]);
         }
     };
     if (wave < full) {
@@ -1181,19 +1174,14 @@ __global__ __launch_bounds__(kFewWaves * kWave) void linear_few_kernel(LinearPar
         for (int h = 0; h < 2; ++h) {
             const bool ok = s + q * 16 + h * 8 < K;
             const int o = ok ? s + h * 8 : -q * 16;          // a lane past the end reads its row's start
-            uintx4 wv = *(const uintx4 *)(w + o);
+            uintx4 wv = *(const uintx4 *)(w + o), xv = *(const uintx4 *)(x + o);
             wv = ok ? wv : uintx4{0, 0, 0, 0};
-#pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                uintx4 xv = *(const uintx4 *)(x[i] + o);
-                xv = ok ? xv : uintx4{0, 0, 0, 0};
-                mma(wv, xv, i);
-            }
+            xv = ok ? xv : uintx4{0, 0, 0, 0};
+            mma(wv, xv);
         }
     }
-    // lane l: row l % 16 of x's block, columns (l / 16) 4 + r
-#pragma unroll
-    for (int i = 0; i < MT; ++i) *(floatx4 *)&red[wave][i * 16 + r16][q * 4] = acc[i];
+    // lane l: row l % 16 of x, columns (l / 16) 4 + r
+    *(floatx4 *)&red[wave][r16][q * 4] = acc;
     __syncthreads();
     // a thread of the first waves finishes 8 columns of a row
     const int groups = glu ? 1 : 2, m = threadIdx.x / groups, g = threadIdx.x % groups;
