@@ -35,7 +35,7 @@ struct FinishParams {
     float limit;              // SwiGLU clamp, +inf for none
 };
 
-// How the widest tile's work is spread over the CUs (wide_cut in linear.hip): the
+// How the widest tile's work is spread over the CUs (wide_cut in linear_plan.hpp): the
 // first `whole` tiles in one piece; each of the `rest` others in `parts` of `main`
 // reduction values and a tail, which the first `tails` of them take in one piece,
 // the others in `cuts` of `cut` values.  rest = 0: every tile in one piece.
